@@ -159,6 +159,16 @@ int32_t ep_mxfp8_pack(const uint16_t* x, int64_t rows, int64_t hidden, uint8_t* 
 int32_t ep_nvfp4_unpack(const uint8_t* packed, int64_t rows_in, int64_t hidden,
                         const int32_t* src_row, int64_t rows_out, uint16_t* out, void* stream);
 
+/* MXFP8 rows -> BF16: out = E4M3(data) * 2^(scale - 127), rounded to BF16 (an
+ * exact value unless it falls below BF16's subnormals or past its largest; a
+ * scale byte of 255 or an E4M3 NaN gives NaN).  Reads what ep_mxfp8_pack,
+ * swiglu_mxfp8_checkpoint and ep_mxfp8_direct_receive write.
+ *   data [rows, hidden], scales [rows, hidden/32], out [rows, hidden] BF16.
+ *   Requires hidden a positive multiple of 32, at most 2^24, and
+ *   rows * hidden < 2^34 (EP_ERR_RANGE). */
+int32_t ep_mxfp8_unpack(const uint8_t* data, const uint8_t* scales, int64_t rows, int64_t hidden,
+                        uint16_t* out, void* stream);
+
 /* ---------------------------------------------------------------- routing */
 
 /* Local routing permutation (P2, review comments: routing prepared once and
@@ -467,6 +477,91 @@ int32_t dswiglu_nvfp4_quant_noalloc(const uint16_t* preact, const uint16_t* dy, 
                                     const int32_t* counts, int64_t num_experts, uint16_t* dx, float* amax,
                                     uint8_t* row_codes, uint8_t* row_scales, float* row_scale,
                                     uint8_t* col_codes, uint8_t* col_scales, float* col_scale, void* stream);
+
+/* ---------------------------------------------------------------- BF16 dispatch and combine */
+
+/* Token rows to their experts and back in BF16, for the layers and gradients
+ * that are not quantized (P2, review comments: one routing, prepared once, is
+ * used by the dispatch and by the combine).  All three take the maps of
+ * ep_route_plan; every width from 1 to 2^20 is taken and no row needs an
+ * alignment; fewer than 2^25 tokens and grouped rows, top_k <= 1024 and
+ * tokens * top_k < 2^29 (EP_ERR_RANGE).
+ *
+ * ep_bf16_dispatch: out[g] = x[src_row[g]]; a zero row where src_row[g] is
+ * outside [0, tokens).  Every row below r_cap is written.
+ *   x [tokens, hidden], src_row [r_cap], out [r_cap, hidden]. */
+int32_t ep_bf16_dispatch(const uint16_t* x, int64_t tokens, int64_t hidden, int64_t r_cap,
+                         const int32_t* src_row, uint16_t* out, void* stream);
+
+/* ep_bf16_combine: out[t] = sum over j of weights[t, j] * rows[dst_row[t, j]],
+ * accumulated in FP32 in the order of j and rounded once to BF16.  A slot whose
+ * dst_row is outside [0, r_cap) adds nothing (its weight is not used); a token
+ * with none left gets a zero row; rows that no slot names are not read.
+ * weights NULL: every weight is 1, which makes it the gradient of
+ * ep_bf16_dispatch.
+ *   rows [r_cap, hidden], dst_row [tokens, top_k], weights [tokens, top_k]
+ *   FP32 or NULL, out [tokens, hidden]. */
+int32_t ep_bf16_combine(const uint16_t* rows, int64_t r_cap, int64_t hidden, int64_t tokens, int64_t top_k,
+                        const int32_t* dst_row, const float* weights, uint16_t* out, void* stream);
+
+/* ep_bf16_combine_bwd: the gradients of ep_bf16_combine,
+ *   drows[dst_row[t, j]] = weights[t, j] * dout[t]          (BF16, one rounding)
+ *   dweights[t, j] = sum over h of dout[t, h] * rows[dst_row[t, j], h]  (FP32)
+ * for slots whose dst_row lies in [0, r_cap); dweights is 0 for the others, and
+ * grouped rows whose src_row is outside [0, tokens) (padding) get a zero drows
+ * row: with a plan's maps every row below r_cap is written, by one writer, and
+ * results do not depend on timing.
+ *   dout [tokens, hidden], rows and drows [r_cap, hidden], dst_row and weights
+ *   and dweights [tokens, top_k], src_row [r_cap]. */
+int32_t ep_bf16_combine_bwd(const uint16_t* dout, const uint16_t* rows, int64_t tokens, int64_t hidden,
+                            int64_t top_k, int64_t r_cap, const int32_t* dst_row, const int32_t* src_row,
+                            const float* weights, uint16_t* drows, float* dweights, void* stream);
+
+/* ---------------------------------------------------------------- products with NVFP4 weights */
+
+/* Few token rows times the NVFP4 weights of their experts (an expert layer that
+ * serves single tokens or small batches):
+ *   y[t, j] = W[topk_idx[t, j]] x[t]           (x_per_entry 0: x [tokens, hidden])
+ *   y[t, j] = W[topk_idx[t, j]] x[t, j]        (else: x [tokens, top_k, hidden])
+ * W [num_experts, width] rows of NVFP4 over hidden, as ep_nvfp4_pack writes them
+ * ([hidden/2 | hidden/16 | FP32 t] bytes, stride 9*hidden/16 + 4; value =
+ * e2m1 * s_b * t).  Decoded weights and their products with BF16 are exact;
+ * sums are FP32, in an order fixed by the sizes; one rounding to BF16.
+ * swiglu: the width rows are [gate | up] halves and the output is
+ * silu(y_gate) * y_up (taken in FP32, before the rounding), width/2 columns.
+ * An entry -1 gives a zero row; another id outside [0, num_experts) too, and
+ * sets EP_DEVERR_EXPERT_ID in *d_error (d_error may be NULL).  No row of x that
+ * only such entries name is read.
+ *   topk_idx [tokens, top_k] int32 or int64 (idx_dtype); NULL: one dense matrix
+ *   (num_experts and top_k 1).  out [tokens, top_k, width or width/2] BF16.
+ *   Requires hidden a positive multiple of 64, at most 2^20; 1 <= num_experts
+ *   <= 1024; 1 <= width <= 2^24, even with swiglu; tokens * top_k <= 4096
+ *   (EP_ERR_RANGE: larger batches are a matrix product's). */
+int32_t ep_nvfp4_expert_matvec(const uint16_t* x, int64_t tokens, int64_t hidden, int32_t x_per_entry,
+                               const uint8_t* weight, int64_t num_experts, int64_t width,
+                               const void* topk_idx, int32_t idx_dtype, int64_t top_k, int32_t swiglu,
+                               uint16_t* out, int32_t* d_error, void* stream);
+
+/* ---------------------------------------------------------------- SwiGLU with an 8-bit checkpoint */
+
+/* SwiGLU whose pre-activation is kept in MXFP8 for the backward pass (33 bytes
+ * per 32 values instead of 64):
+ *   act = silu(a) * b of the BF16 preact = [a | b], computed in FP32 and rounded
+ *   to BF16; data and scales: the bytes ep_mxfp8_pack gives for preact.
+ *   preact [tokens, 2*ffn], act [tokens, ffn], data [tokens, 2*ffn], scales
+ *   [tokens, 2*ffn/32].  Requires ffn a positive multiple of 32, at most 2^24,
+ *   and tokens * ffn < 2^34 (EP_ERR_RANGE). */
+int32_t swiglu_mxfp8_checkpoint(const uint16_t* preact, int64_t tokens, int64_t ffn, uint16_t* act,
+                                uint8_t* data, uint8_t* scales, void* stream);
+
+/* The gradient from that checkpoint: a and b are its decoded values,
+ *   dx = [dy*b*s*(1 + a*(1-s)) | dy*a*s], s = sigmoid(a), in FP32, rounded to
+ *   BF16 (dswiglu_nvfp4_quant's dx); act = silu(a) * b again, for the second
+ *   product's weight gradient (not written if NULL).
+ *   dy [tokens, ffn], dx [tokens, 2*ffn], act [tokens, ffn] or NULL; sizes as
+ *   for swiglu_mxfp8_checkpoint. */
+int32_t dswiglu_mxfp8_checkpoint(const uint8_t* data, const uint8_t* scales, const uint16_t* dy, int64_t tokens,
+                                 int64_t ffn, uint16_t* dx, uint16_t* act, void* stream);
 
 #ifdef __cplusplus
 }

@@ -58,6 +58,13 @@ _SIGS = {
     "ep_nvfp4_direct_receive_sr_stream": (_I32, [_P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "ep_nvfp4_pack_scatter": (_I32, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _P, _P, _P]),
     "ep_nvfp4_columnwise_grouped": (_I32, [_P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P]),
+    "ep_mxfp8_unpack": (_I32, [_P, _P, _I64, _I64, _P, _P]),
+    "ep_bf16_dispatch": (_I32, [_P, _I64, _I64, _I64, _P, _P, _P]),
+    "ep_bf16_combine": (_I32, [_P, _I64, _I64, _I64, _I64, _P, _P, _P, _P]),
+    "ep_bf16_combine_bwd": (_I32, [_P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P]),
+    "ep_nvfp4_expert_matvec": (_I32, [_P, _I64, _I64, _I32, _P, _I64, _I64, _P, _I32, _I64, _I32, _P, _P, _P]),
+    "swiglu_mxfp8_checkpoint": (_I32, [_P, _I64, _I64, _P, _P, _P, _P]),
+    "dswiglu_mxfp8_checkpoint": (_I32, [_P, _P, _P, _I64, _I64, _P, _P, _P]),
     "dswiglu_nvfp4_quant": (_I32, [_P, _P, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "dswiglu_nvfp4_quant_sr": (_I32, [_P, _P, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P]),
     "dswiglu_nvfp4_quant_sr_stream": (_I32, [_P, _P, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P,
@@ -99,6 +106,18 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(dev):
     return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _launch(dev, name, *args):
+    """Calls entry point ``name`` on ``dev`` and its current stream; addresses are
+    plain integers (None: NULL).  The device is switched only when another one is
+    current: for a single token's rows the host's time is the call's."""
+    if torch.cuda.current_device() == dev.index:
+        status = getattr(lib(), name)(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(lib(), name)(*args, torch.cuda.current_stream(dev).cuda_stream)
+    _check(status, name)
 
 
 def _dev(t):
@@ -252,6 +271,27 @@ def ep_mxfp8_pack(x, out=None):
     with torch.cuda.device(dev):
         _check(lib().ep_mxfp8_pack(_ptr(x), t, h, _ptr(data), _ptr(scales), _stream(dev)), "ep_mxfp8_pack")
     return data, scales, out
+
+
+def _mxfp8(data, scales):
+    """Device and sizes of MXFP8 rows: data [rows, hidden], scales [rows, hidden/32]."""
+    dev = _dev(data)
+    _need(data, torch.uint8, "data")
+    if data.dim() != 2 or data.shape[1] % 32:
+        raise ValueError("data must be [rows, hidden] with hidden a multiple of 32")
+    rows, hidden = data.shape
+    _need(scales, torch.uint8, "scales", dev, shape=(rows, hidden // 32))
+    return dev, rows, hidden
+
+
+def ep_mxfp8_unpack(data, scales, out=None):
+    """MXFP8 rows (data uint8 [T, H], scales uint8 [T, H/32]) -> BF16 [T, H]."""
+    dev, t, h = _mxfp8(data, scales)
+    if out is None:
+        out = torch.empty((t, h), dtype=torch.bfloat16, device=dev)
+    _need(out, torch.bfloat16, "out", dev, shape=(t, h))
+    _launch(dev, "ep_mxfp8_unpack", data.data_ptr(), scales.data_ptr(), t, h, out.data_ptr())
+    return out
 
 
 # ------------------------------------------------------------------ routing / receive
@@ -549,6 +589,165 @@ def ep_mxfp8_direct_receive(data, scales, plan, out=None):
         _check(lib().ep_mxfp8_direct_receive(_ptr(data), _ptr(scales), t, h, r_cap, _ptr(plan["src_row"]),
                                              _ptr(out[0]), _ptr(out[1]), _stream(dev)), "ep_mxfp8_direct_receive")
     return out
+
+
+# ------------------------------------------------------------------ BF16 dispatch / combine
+def _rows(t, name, rows=None, hidden=None, dev=None):
+    """A BF16 matrix of rows, with the sizes given."""
+    _need(t, torch.bfloat16, name, dev)
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (hidden is not None and t.shape[1] != hidden):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{'rows' if rows is None else rows}, "
+                         f"{'hidden' if hidden is None else hidden}]")
+
+
+def _slots(plan, dev):
+    """Sizes of a plan whose maps both ways are used: r_cap, tokens, top_k."""
+    _, r_cap = _plan(plan, dev)
+    if plan["dst_row"].dim() != 2:
+        raise ValueError("plan dst_row must be [tokens, top_k]")
+    return r_cap, plan["dst_row"].shape[0], plan["dst_row"].shape[1]
+
+
+def ep_bf16_dispatch(x, plan, out=None):
+    """BF16 token rows [T, H] copied into the grouped rows of a routing plan:
+    BF16 [r_cap, H], padding rows zero.  Its gradient is ``ep_bf16_combine``
+    without weights."""
+    dev = _dev(x)
+    _rows(x, "x")
+    t, h = x.shape
+    _, r_cap = _plan(plan, dev, tokens=t)
+    if out is None:
+        out = torch.empty((r_cap, h), dtype=torch.bfloat16, device=dev)
+    _rows(out, "out", r_cap, h, dev)
+    _launch(dev, "ep_bf16_dispatch", x.data_ptr(), t, h, r_cap, plan["src_row"].data_ptr(), out.data_ptr())
+    return out
+
+
+def ep_bf16_combine(rows, plan, weights=None, out=None):
+    """Grouped BF16 rows [r_cap, H] back to their tokens: out[t] = sum over slots j
+    of weights[t, j] * rows[dst_row[t, j]] (FP32 sum, BF16 [T, H]); ``weights``
+    float32 [T, k], or None for a plain sum (the gradient of ``ep_bf16_dispatch``).
+    Unused slots add nothing; padding rows are not read."""
+    dev = _dev(rows)
+    r_cap, t, k = _slots(plan, dev)
+    _rows(rows, "rows", rows=r_cap)
+    h = rows.shape[1]
+    if weights is not None:
+        _need(weights, torch.float32, "weights", dev, shape=(t, k))
+    if out is None:
+        out = torch.empty((t, h), dtype=torch.bfloat16, device=dev)
+    _rows(out, "out", t, h, dev)
+    _launch(dev, "ep_bf16_combine", rows.data_ptr(), r_cap, h, t, k, plan["dst_row"].data_ptr(),
+            None if weights is None else weights.data_ptr(), out.data_ptr())
+    return out
+
+
+def ep_bf16_combine_bwd(dout, rows, plan, weights, drows=None, dweights=None):
+    """Gradients of ``ep_bf16_combine`` for dout BF16 [T, H]: (drows BF16 [r_cap, H],
+    padding rows zero; dweights float32 [T, k], 0 for unused slots)."""
+    dev = _dev(dout)
+    r_cap, t, k = _slots(plan, dev)
+    _rows(dout, "dout", rows=t)
+    h = dout.shape[1]
+    _rows(rows, "rows", r_cap, h, dev)
+    _need(weights, torch.float32, "weights", dev, shape=(t, k))
+    if drows is None:
+        drows = torch.empty((r_cap, h), dtype=torch.bfloat16, device=dev)
+    if dweights is None:
+        dweights = torch.empty((t, k), dtype=torch.float32, device=dev)
+    _rows(drows, "drows", r_cap, h, dev)
+    _need(dweights, torch.float32, "dweights", dev, shape=(t, k))
+    _launch(dev, "ep_bf16_combine_bwd", dout.data_ptr(), rows.data_ptr(), t, h, k, r_cap, plan["dst_row"].data_ptr(),
+            plan["src_row"].data_ptr(), weights.data_ptr(), drows.data_ptr(), dweights.data_ptr())
+    return drows, dweights
+
+
+# ------------------------------------------------------------------ products with NVFP4 weights
+def ep_nvfp4_expert_matvec(x, weight, topk_idx=None, swiglu=False, out=None, d_error=None):
+    """Few token rows times the NVFP4 weights of their experts, for serving single
+    tokens and small batches.
+
+    ``weight``: uint8 [E, N, 9K/16 + 4], rows of K weights as ``ep_nvfp4_pack``
+    writes them.  ``topk_idx`` [T, k] (int32 or int64; -1: unused slot, zero row).
+    ``x``: BF16 [T, K], or [T, k, K] with a row of its own for each entry.
+    Returns BF16 [T, k, N]; with ``swiglu`` the N rows are [gate | up] halves and
+    the result is silu(gate) * up, [T, k, N/2].  Without ``topk_idx``, ``weight`` is
+    one matrix [N, 9K/16 + 4] and the result [T, N] (or [T, N/2]).  ``d_error``:
+    optional device int32 [1], OR-ed with EP_DEVERR_EXPERT_ID on a bad id."""
+    dev = _dev(x)
+    _need(x, torch.bfloat16, "x")
+    _need(weight, torch.uint8, "weight", dev)
+    dense = topk_idx is None
+    if x.dim() not in ((2,) if dense else (2, 3)):
+        raise ValueError("x must be [tokens, hidden]" + ("" if dense else " or [tokens, top_k, hidden]"))
+    t, h = x.shape[0], x.shape[-1]
+    rb = _row_bytes(h, "ep_nvfp4_expert_matvec")
+    if weight.dim() != (2 if dense else 3) or weight.shape[-1] != rb:
+        raise ValueError(f"weight has shape {tuple(weight.shape)}, expected [{'' if dense else 'experts, '}width, {rb}] "
+                         f"for hidden {h}")
+    e, n = (1 if dense else weight.shape[0]), weight.shape[-2]
+    if swiglu and n % 2:
+        raise ValueError("swiglu needs an even number of weight rows ([gate | up])")
+    k, idt, ids = 1, EP_IDX_INT32, None
+    if not dense:
+        idt = _topk(topk_idx)
+        k, ids = topk_idx.shape[1], topk_idx.data_ptr()
+        if topk_idx.device != dev or topk_idx.shape[0] != t or (x.dim() == 3 and x.shape[1] != k):
+            raise ValueError(f"topk_idx must be [tokens, top_k] on {dev}, as x {tuple(x.shape)} has them")
+    width = n // 2 if swiglu else n
+    shape = (t, width) if dense else (t, k, width)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    _need(out, torch.bfloat16, "out", dev, shape=shape)
+    if d_error is not None:
+        _need(d_error, torch.int32, "d_error", dev, numel=1)
+    _launch(dev, "ep_nvfp4_expert_matvec", x.data_ptr(), t, h, int(x.dim() == 3), weight.data_ptr(), e, n, ids, idt, k,
+            int(swiglu), out.data_ptr(), None if d_error is None else d_error.data_ptr())
+    return out
+
+
+# ------------------------------------------------------------------ SwiGLU with an 8-bit checkpoint
+def swiglu_mxfp8_checkpoint(preact, act=None, data=None, scales=None):
+    """act = silu(a) * b of BF16 preact [T, 2F] = [a | b], and preact kept as MXFP8
+    (the bytes of ``ep_mxfp8_pack``): (act BF16 [T, F], data uint8 [T, 2F], scales
+    uint8 [T, 2F/32])."""
+    dev = _dev(preact)
+    _need(preact, torch.bfloat16, "preact")
+    if preact.dim() != 2 or preact.shape[1] % 64:
+        raise ValueError("preact must be [tokens, 2*ffn] with ffn a multiple of 32")
+    t, f2 = preact.shape
+    if act is None:
+        act = torch.empty((t, f2 // 2), dtype=torch.bfloat16, device=dev)
+    if data is None:
+        data = torch.empty((t, f2), dtype=torch.uint8, device=dev)
+    if scales is None:
+        scales = torch.empty((t, f2 // 32), dtype=torch.uint8, device=dev)
+    _need(act, torch.bfloat16, "act", dev, shape=(t, f2 // 2))
+    _need(data, torch.uint8, "data", dev, shape=(t, f2))
+    _need(scales, torch.uint8, "scales", dev, shape=(t, f2 // 32))
+    _launch(dev, "swiglu_mxfp8_checkpoint", preact.data_ptr(), t, f2 // 2, act.data_ptr(), data.data_ptr(),
+            scales.data_ptr())
+    return act, data, scales
+
+
+def dswiglu_mxfp8_checkpoint(data, scales, dy, dx=None, act=None, need_act=True):
+    """The gradient of SwiGLU from its 8-bit checkpoint: (dx BF16 [T, 2F] = [da | db],
+    act BF16 [T, F] computed again from the checkpoint, or None with
+    ``need_act=False``)."""
+    dev, t, f2 = _mxfp8(data, scales)
+    if f2 % 64:
+        raise ValueError("data must be [tokens, 2*ffn] with ffn a multiple of 32")
+    _need(dy, torch.bfloat16, "dy", dev, shape=(t, f2 // 2))
+    if dx is None:
+        dx = torch.empty((t, f2), dtype=torch.bfloat16, device=dev)
+    _need(dx, torch.bfloat16, "dx", dev, shape=(t, f2))
+    if act is None and need_act:
+        act = torch.empty((t, f2 // 2), dtype=torch.bfloat16, device=dev)
+    if act is not None:
+        _need(act, torch.bfloat16, "act", dev, shape=(t, f2 // 2))
+    _launch(dev, "dswiglu_mxfp8_checkpoint", data.data_ptr(), scales.data_ptr(), dy.data_ptr(), t, f2 // 2,
+            dx.data_ptr(), None if act is None else act.data_ptr())
+    return dx, act
 
 
 # ------------------------------------------------------------------ dSwiGLU

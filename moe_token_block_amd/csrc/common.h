@@ -32,6 +32,15 @@ __device__ __forceinline__ uint4 ld_stream16(const void* p) {
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
+// A value at any byte address (rows of an odd width, views that start anywhere):
+// global memory accesses need no alignment, so the instruction is the same.
+template <typename T>
+struct __attribute__((packed)) AnyAddr { T v; };
+template <typename T>
+__device__ __forceinline__ T ld_any(const void* p) { return reinterpret_cast<const AnyAddr<T>*>(p)->v; }
+template <typename T>
+__device__ __forceinline__ void st_any(void* p, T v) { reinterpret_cast<AnyAddr<T>*>(p)->v = v; }
+
 // Compile-time loop: f(std::integral_constant<int, I>) for I = B .. E-1, each
 // body its own straight-line copy.  For loops whose bodies are too large for
 // the compiler to unroll by itself: a loop left rolled indexes its register
@@ -50,6 +59,14 @@ constexpr float kTokenBound = 2688.0f;  // 6 * 448
 // ----------------------------------------------------------------- bit casts
 __device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Two floats rounded to BF16, the first in the low half.
+__device__ __forceinline__ uint32_t bf16pair(float a, float b) {
+  bf16x2 r;
+  r[0] = (__bf16)a;
+  r[1] = (__bf16)b;
+  return __builtin_bit_cast(uint32_t, r);
+}
 
 // Power of two 2^k as a float, k in [-126, 127] (normal range only).
 __device__ __forceinline__ float pow2f(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }

@@ -130,13 +130,6 @@ __device__ __forceinline__ void dswiglu_pair(float a, float b, float dy, float& 
   db = dy * silu;
 }
 
-__device__ __forceinline__ uint32_t bf16pair(float a, float b) {
-  bf16x2 r;
-  r[0] = (__bf16)a;
-  r[1] = (__bf16)b;
-  return __builtin_bit_cast(uint32_t, r);
-}
-
 // One wave per row; lane l owns 8-column chunks j = l + 64k of a, b and dy,
 // NB of them per group.  A group's 3 * NB loads are issued before any of its
 // arithmetic (chunks past the row's end load its last chunk and are not

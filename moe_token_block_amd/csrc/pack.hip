@@ -14,6 +14,7 @@
 
 #include "common.h"
 #include "launch.h"
+#include "mxfp8.h"
 
 namespace mtb {
 
@@ -417,32 +418,6 @@ __global__ __launch_bounds__(256) void k_nvfp4_pack_sr_rows(const uint16_t* __re
 // ----------------------------------------------------------------- MXFP8
 // Two lanes per 32-element block (16 elements each): one xor-1 exchange gives
 // the block max.  Data goes out as one 16-byte store per lane.
-__device__ __forceinline__ int mx_exponent(float a) {
-  if (!(a > 0.0f)) return 0;
-  int sub = 0;
-  if (a < 0x1p-126f) { a *= 0x1p64f; sub = 64; }
-  int E = __builtin_amdgcn_frexp_expf(a) - 1 - sub;
-  float m = __builtin_amdgcn_frexp_mantf(a) * 2.0f;
-  int e = E - 8 + (m > 1.75f ? 1 : 0);  // least e with a <= 448 * 2^e
-  return e < -127 ? -127 : (e > 127 ? 127 : e);
-}
-
-__device__ __forceinline__ uint32_t fp8x4_from_bf16(uint32_t w0, uint32_t w1, float scale) {
-  i16x2 r = {0, 0};
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2, w0), scale, false);
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2, w1), scale, true);
-  return __builtin_bit_cast(uint32_t, r);
-}
-
-// Tiny blocks (e < -126): scale the inputs by 2^64 first so that the
-// converter's power of two stays a normal float.
-__device__ __forceinline__ uint32_t fp8x4_from_bf16_tiny(uint32_t w0, uint32_t w1, float scale) {
-  i16x2 r = {0, 0};
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, bf16lo(w0) * 0x1p64f, bf16hi(w0) * 0x1p64f, scale, false);
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, bf16lo(w1) * 0x1p64f, bf16hi(w1) * 0x1p64f, scale, true);
-  return __builtin_bit_cast(uint32_t, r);
-}
-
 __global__ __launch_bounds__(256) void k_mxfp8_pack(const uint16_t* __restrict__ x, int64_t total_chunks,
                                                     int /* H: chunks run over the whole tensor */,
                                                     uint8_t* __restrict__ data,

@@ -12,13 +12,6 @@
 
 namespace mtb {
 
-__device__ __forceinline__ uint32_t bf16pair(float a, float b) {
-  bf16x2 r;
-  r[0] = (__bf16)a;
-  r[1] = (__bf16)b;
-  return __builtin_bit_cast(uint32_t, r);
-}
-
 // 8 E2M1 codes of word w (4 bytes) times the block multiplier -> 4 packed BF16 pairs.
 __device__ __forceinline__ void decode8(uint32_t w, float scale, float mant, uint32_t* o) {
   f32x2 p0 = fp4_unpack2<0>(w, scale), p1 = fp4_unpack2<1>(w, scale);

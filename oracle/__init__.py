@@ -32,4 +32,4 @@ something other than itself, except the choice of the RHT sign vector (an
 arbitrary fixed constant by design) -- parity unpinned for that choice only.
 """
 
-from . import formats, philox, nvfp4, mxfp8, mxfp4, routing, rht, receive, dswiglu  # noqa: F401
+from . import formats, philox, nvfp4, mxfp8, mxfp4, routing, rht, receive, dswiglu, expert  # noqa: F401
