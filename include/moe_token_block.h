@@ -484,14 +484,16 @@ int32_t dswiglu_nvfp4_quant_noalloc(const uint16_t* preact, const uint16_t* dy, 
  * that are not quantized (P2, review comments: one routing, prepared once, is
  * used by the dispatch and by the combine).  All three take the maps of
  * ep_route_plan; every width from 1 to 2^20 is taken and no row needs an
- * alignment; fewer than 2^25 tokens and grouped rows, top_k <= 1024 and
- * tokens * top_k < 2^29 (EP_ERR_RANGE).
+ * alignment; fewer than 2^23 tokens and 2^25 grouped rows, top_k <= 1024,
+ * tokens * top_k < 2^29 and tokens * ceil(hidden/512) < 2^25 (EP_ERR_RANGE).
  *
- * ep_bf16_dispatch: out[g] = x[src_row[g]]; a zero row where src_row[g] is
- * outside [0, tokens).  Every row below r_cap is written.
- *   x [tokens, hidden], src_row [r_cap], out [r_cap, hidden]. */
-int32_t ep_bf16_dispatch(const uint16_t* x, int64_t tokens, int64_t hidden, int64_t r_cap,
-                         const int32_t* src_row, uint16_t* out, void* stream);
+ * ep_bf16_dispatch: out[dst_row[t, j]] = x[t] for every slot whose dst_row lies
+ * in [0, r_cap), and zero rows where src_row is outside [0, tokens): with a
+ * plan's maps every row below r_cap is written, once.
+ *   x [tokens, hidden], dst_row [tokens, top_k], src_row [r_cap], out [r_cap,
+ *   hidden]. */
+int32_t ep_bf16_dispatch(const uint16_t* x, int64_t tokens, int64_t hidden, int64_t top_k, int64_t r_cap,
+                         const int32_t* dst_row, const int32_t* src_row, uint16_t* out, void* stream);
 
 /* ep_bf16_combine: out[t] = sum over j of weights[t, j] * rows[dst_row[t, j]],
  * accumulated in FP32 in the order of j and rounded once to BF16.  A slot whose

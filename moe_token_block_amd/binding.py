@@ -59,7 +59,7 @@ _SIGS = {
     "ep_nvfp4_pack_scatter": (_I32, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _P, _P, _P]),
     "ep_nvfp4_columnwise_grouped": (_I32, [_P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P]),
     "ep_mxfp8_unpack": (_I32, [_P, _P, _I64, _I64, _P, _P]),
-    "ep_bf16_dispatch": (_I32, [_P, _I64, _I64, _I64, _P, _P, _P]),
+    "ep_bf16_dispatch": (_I32, [_P, _I64, _I64, _I64, _I64, _P, _P, _P, _P]),
     "ep_bf16_combine": (_I32, [_P, _I64, _I64, _I64, _I64, _P, _P, _P, _P]),
     "ep_bf16_combine_bwd": (_I32, [_P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P]),
     "ep_nvfp4_expert_matvec": (_I32, [_P, _I64, _I64, _I32, _P, _I64, _I64, _P, _I32, _I64, _I32, _P, _P, _P]),
@@ -613,13 +613,14 @@ def ep_bf16_dispatch(x, plan, out=None):
     BF16 [r_cap, H], padding rows zero.  Its gradient is ``ep_bf16_combine``
     without weights."""
     dev = _dev(x)
-    _rows(x, "x")
-    t, h = x.shape
-    _, r_cap = _plan(plan, dev, tokens=t)
+    r_cap, t, k = _slots(plan, dev)
+    _rows(x, "x", rows=t)
+    h = x.shape[1]
     if out is None:
         out = torch.empty((r_cap, h), dtype=torch.bfloat16, device=dev)
     _rows(out, "out", r_cap, h, dev)
-    _launch(dev, "ep_bf16_dispatch", x.data_ptr(), t, h, r_cap, plan["src_row"].data_ptr(), out.data_ptr())
+    _launch(dev, "ep_bf16_dispatch", x.data_ptr(), t, h, k, r_cap, plan["dst_row"].data_ptr(),
+            plan["src_row"].data_ptr(), out.data_ptr())
     return out
 
 

@@ -27,16 +27,19 @@ def lib():
 @pytest.mark.skipif(torch.cuda.is_available(), reason="passes fake pointers: only where no GPU exists")
 def test_validation_before_launch(lib):
     P, N = ctypes.c_void_p(0x1000), None         # never dereferenced: every call below fails validation or does nothing
-    assert lib.ep_bf16_dispatch(P, 4, 0, 8, P, P, N) == -2
-    assert lib.ep_bf16_dispatch(P, -1, 8, 8, P, P, N) == -2
-    assert lib.ep_bf16_dispatch(P, 4, 8, 1 << 25, P, P, N) == -8
-    assert lib.ep_bf16_dispatch(P, 4, (1 << 20) + 1, 8, P, P, N) == -8
-    assert lib.ep_bf16_dispatch(P, 4, 8, 8, N, P, N) == -1
-    assert lib.ep_bf16_dispatch(N, 4, 8, 8, P, P, N) == -1
-    assert lib.ep_bf16_dispatch(N, 0, 8, 0, N, N, N) == 0
+    assert lib.ep_bf16_dispatch(P, 4, 0, 2, 8, P, P, P, N) == -2
+    assert lib.ep_bf16_dispatch(P, -1, 8, 2, 8, P, P, P, N) == -2
+    assert lib.ep_bf16_dispatch(P, 4, 8, 0, 8, P, P, P, N) == -2
+    assert lib.ep_bf16_dispatch(P, 4, 8, 2, 1 << 25, P, P, P, N) == -8
+    assert lib.ep_bf16_dispatch(P, 1 << 23, 8, 2, 8, P, P, P, N) == -8
+    assert lib.ep_bf16_dispatch(P, 4, (1 << 20) + 1, 2, 8, P, P, P, N) == -8
+    assert lib.ep_bf16_dispatch(P, 4, 8, 2, 8, P, N, P, N) == -1
+    assert lib.ep_bf16_dispatch(P, 4, 8, 2, 8, N, P, P, N) == -1
+    assert lib.ep_bf16_dispatch(N, 4, 8, 2, 8, P, P, P, N) == -1
+    assert lib.ep_bf16_dispatch(N, 0, 8, 2, 0, N, N, N, N) == 0
     assert lib.ep_bf16_combine(P, 8, 8, 4, 0, P, P, P, N) == -2
     assert lib.ep_bf16_combine(P, 8, 8, 4, 1025, P, P, P, N) == -8
-    assert lib.ep_bf16_combine(P, 8, 8, 1 << 25, 2, P, P, P, N) == -8
+    assert lib.ep_bf16_combine(P, 8, 8, 1 << 23, 2, P, P, P, N) == -8
     assert lib.ep_bf16_combine(P, 8, 8, 4, 2, N, P, P, N) == -1
     assert lib.ep_bf16_combine(N, 8, 8, 4, 2, P, P, P, N) == -1
     assert lib.ep_bf16_combine(N, 0, 8, 0, 2, N, N, N, N) == 0
@@ -93,9 +96,10 @@ int main(void) {
   const int64_t big[] = {INT64_MAX, INT64_MAX & ~(int64_t)63, INT64_MIN, -1, (int64_t)1 << 62, (int64_t)1 << 32};
   for (int i = 0; i < 6; ++i) {
     const int64_t b = big[i];
-    REFUSED(ep_bf16_dispatch(P, b, 8, 8, P, P, 0));
-    REFUSED(ep_bf16_dispatch(P, 4, b, 8, P, P, 0));
-    REFUSED(ep_bf16_dispatch(P, 4, 8, b, P, P, 0));
+    REFUSED(ep_bf16_dispatch(P, b, 8, 2, 8, P, P, P, 0));
+    REFUSED(ep_bf16_dispatch(P, 4, b, 2, 8, P, P, P, 0));
+    REFUSED(ep_bf16_dispatch(P, 4, 8, b, 8, P, P, P, 0));
+    REFUSED(ep_bf16_dispatch(P, 4, 8, 2, b, P, P, P, 0));
     REFUSED(ep_bf16_combine(P, b, 8, 4, 2, P, P, P, 0));
     REFUSED(ep_bf16_combine(P, 8, 8, b, 2, P, P, P, 0));
     REFUSED(ep_bf16_combine(P, 8, 8, 4, b, P, P, P, 0));
