@@ -205,7 +205,9 @@ MATVEC = [(1, 8, 2, 64, 4096, 0.0, False, True), (1, 1, 1, 1, 64, 0.0, False, Fa
           (2, 3, 2, 33, 192, 0.0, False, False), (5, 2, 2, 50, 1088, 0.2, True, True), (7, 32, 8, 16, 320, 0.1, False, False),
           (16, 2, 1, 40, 256, 0.0, False, True), (17, 3, 2, 35, 704, 0.0, True, False), (33, 2, 2, 24, 576, 0.1, False, True),
           (64, 5, 3, 70, 448, 0.0, False, False), (100, 1, 1, 130, 64, 0.0, False, False), (128, 4, 4, 18, 2048, 0.3, True, True),
-          (3, 7, 4, 260, 7168, 0.0, False, False), (9, 5, 5, 8, 832, 1.0, False, False), (1000, 6, 4, 6, 128, 0.1, False, True)]
+          (3, 7, 4, 260, 7168, 0.0, False, False), (50, 2, 1, 37, 1600, 0.0, False, False), (70, 1, 1, 44, 512, 0.0, True, True),
+          (97, 2, 2, 300, 576, 0.1, False, False), (7, 1, 1, 129, 64, 0.0, False, False), (4, 8, 2, 4098, 640, 0.0, False, True),
+          (9, 2, 2, 18, 4160, 0.0, True, False), (200, 3, 1, 514, 1088, 0.05, False, True), (9, 5, 5, 8, 832, 1.0, False, False), (1000, 6, 4, 6, 128, 0.1, False, True)]
 
 
 @pytest.mark.parametrize("case", MATVEC)
@@ -272,12 +274,13 @@ def test_matvec_special_values_stay_in_their_row(dev):
     _near(_bits(got[keep]), y[keep], (2 * 257 * U * mag)[keep], "other rows")
 
 
-@pytest.mark.parametrize("scale", [2.0 ** -115, 2.0 ** 100])
-def test_matvec_far_from_one(dev, scale):
-    # weight rows and activations at the ends of BF16's range whose products are ordinary numbers
+@pytest.mark.parametrize("scale,x_scale", [(2.0 ** -115, 2.0 ** 115), (2.0 ** 100, 2.0 ** -100), (2.0 ** -128, 2.0 ** 120)])
+def test_matvec_far_from_one(dev, scale, x_scale):
+    # weight rows and activations at the ends of BF16's range (row scales below FP32's normal numbers in the last)
+    # whose products are ordinary numbers
     rng = np.random.default_rng(13)
     w = nvfp4.pack_rows(_bits(rng.standard_normal((24, 192)) * scale)).reshape(1, 24, -1)
-    xb = _bits(rng.standard_normal((3, 192)) / scale)
+    xb = _bits(rng.standard_normal((3, 192)) * x_scale)
     ids = np.zeros((3, 1), dtype=np.int32)
     got = mtb.ep_nvfp4_expert_matvec(bf16_dev(xb, dev), torch.from_numpy(w).to(dev), torch.from_numpy(ids).to(dev))
     _check_matvec(got, expert.f64(xb), w, ids, False, f"scale {scale}")
