@@ -108,16 +108,25 @@ def _stream(dev):
     return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
 
 
+# The current stream's handle without a Stream object around it: 0.1 us of a
+# call's host time instead of 1.9 (a single token's call is bound by the host).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _launch(dev, name, *args):
     """Calls entry point ``name`` on ``dev`` and its current stream; addresses are
     plain integers (None: NULL).  The device is switched only when another one is
-    current: for a single token's rows the host's time is the call's."""
-    if torch.cuda.current_device() == dev.index:
-        status = getattr(lib(), name)(*args, torch.cuda.current_stream(dev).cuda_stream)
+    current."""
+    f = getattr(_lib or lib(), name)
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        status = f(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            status = getattr(lib(), name)(*args, torch.cuda.current_stream(dev).cuda_stream)
-    _check(status, name)
+            status = f(*args, _raw_stream(index))
+    if status:
+        _check(status, name)
 
 
 def _dev(t):
@@ -131,6 +140,9 @@ def _need(t, dtype, name, dev=None, shape=None, numel=None):
     size -- an exact ``shape``, or at least ``numel`` elements.  The C ABI gets
     raw pointers, so this is the only place a buffer too small for the sizes
     passed with it can be caught before a kernel writes past its end."""
+    if (type(t) is torch.Tensor and t.dtype is dtype and numel is None and (shape is None or t.shape == shape)
+            and (dev is None or t.device == dev) and t.is_contiguous()):
+        return  # all in order, in one go: several of these are made for every call
     if not torch.is_tensor(t):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype != dtype:
@@ -289,7 +301,8 @@ def ep_mxfp8_unpack(data, scales, out=None):
     dev, t, h = _mxfp8(data, scales)
     if out is None:
         out = torch.empty((t, h), dtype=torch.bfloat16, device=dev)
-    _need(out, torch.bfloat16, "out", dev, shape=(t, h))
+    else:
+        _need(out, torch.bfloat16, "out", dev, shape=(t, h))
     _launch(dev, "ep_mxfp8_unpack", data.data_ptr(), scales.data_ptr(), t, h, out.data_ptr())
     return out
 
@@ -595,6 +608,8 @@ def ep_mxfp8_direct_receive(data, scales, plan, out=None):
 def _rows(t, name, rows=None, hidden=None, dev=None):
     """A BF16 matrix of rows, with the sizes given."""
     _need(t, torch.bfloat16, name, dev)
+    if t.shape == (rows, hidden):
+        return
     if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (hidden is not None and t.shape[1] != hidden):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{'rows' if rows is None else rows}, "
                          f"{'hidden' if hidden is None else hidden}]")
@@ -617,8 +632,9 @@ def ep_bf16_dispatch(x, plan, out=None):
     _rows(x, "x", rows=t)
     h = x.shape[1]
     if out is None:
-        out = torch.empty((r_cap, h), dtype=torch.bfloat16, device=dev)
-    _rows(out, "out", r_cap, h, dev)
+        out = x.new_empty((r_cap, h))
+    else:
+        _rows(out, "out", r_cap, h, dev)
     _launch(dev, "ep_bf16_dispatch", x.data_ptr(), t, h, k, r_cap, plan["dst_row"].data_ptr(),
             plan["src_row"].data_ptr(), out.data_ptr())
     return out
@@ -636,8 +652,9 @@ def ep_bf16_combine(rows, plan, weights=None, out=None):
     if weights is not None:
         _need(weights, torch.float32, "weights", dev, shape=(t, k))
     if out is None:
-        out = torch.empty((t, h), dtype=torch.bfloat16, device=dev)
-    _rows(out, "out", t, h, dev)
+        out = rows.new_empty((t, h))
+    else:
+        _rows(out, "out", t, h, dev)
     _launch(dev, "ep_bf16_combine", rows.data_ptr(), r_cap, h, t, k, plan["dst_row"].data_ptr(),
             None if weights is None else weights.data_ptr(), out.data_ptr())
     return out
@@ -653,11 +670,13 @@ def ep_bf16_combine_bwd(dout, rows, plan, weights, drows=None, dweights=None):
     _rows(rows, "rows", r_cap, h, dev)
     _need(weights, torch.float32, "weights", dev, shape=(t, k))
     if drows is None:
-        drows = torch.empty((r_cap, h), dtype=torch.bfloat16, device=dev)
+        drows = rows.new_empty((r_cap, h))
+    else:
+        _rows(drows, "drows", r_cap, h, dev)
     if dweights is None:
-        dweights = torch.empty((t, k), dtype=torch.float32, device=dev)
-    _rows(drows, "drows", r_cap, h, dev)
-    _need(dweights, torch.float32, "dweights", dev, shape=(t, k))
+        dweights = weights.new_empty((t, k))
+    else:
+        _need(dweights, torch.float32, "dweights", dev, shape=(t, k))
     _launch(dev, "ep_bf16_combine_bwd", dout.data_ptr(), rows.data_ptr(), t, h, k, r_cap, plan["dst_row"].data_ptr(),
             plan["src_row"].data_ptr(), weights.data_ptr(), drows.data_ptr(), dweights.data_ptr())
     return drows, dweights
@@ -682,7 +701,7 @@ def ep_nvfp4_expert_matvec(x, weight, topk_idx=None, swiglu=False, out=None, d_e
     if x.dim() not in ((2,) if dense else (2, 3)):
         raise ValueError("x must be [tokens, hidden]" + ("" if dense else " or [tokens, top_k, hidden]"))
     t, h = x.shape[0], x.shape[-1]
-    rb = _row_bytes(h, "ep_nvfp4_expert_matvec")
+    rb = 9 * (h // 16) + 4 if h % 64 == 0 and h > 0 else _row_bytes(h, "ep_nvfp4_expert_matvec")
     if weight.dim() != (2 if dense else 3) or weight.shape[-1] != rb:
         raise ValueError(f"weight has shape {tuple(weight.shape)}, expected [{'' if dense else 'experts, '}width, {rb}] "
                          f"for hidden {h}")
@@ -698,8 +717,9 @@ def ep_nvfp4_expert_matvec(x, weight, topk_idx=None, swiglu=False, out=None, d_e
     width = n // 2 if swiglu else n
     shape = (t, width) if dense else (t, k, width)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    _need(out, torch.bfloat16, "out", dev, shape=shape)
+        out = x.new_empty(shape)
+    else:
+        _need(out, torch.bfloat16, "out", dev, shape=shape)
     if d_error is not None:
         _need(d_error, torch.int32, "d_error", dev, numel=1)
     _launch(dev, "ep_nvfp4_expert_matvec", x.data_ptr(), t, h, int(x.dim() == 3), weight.data_ptr(), e, n, ids, idt, k,
@@ -718,14 +738,17 @@ def swiglu_mxfp8_checkpoint(preact, act=None, data=None, scales=None):
         raise ValueError("preact must be [tokens, 2*ffn] with ffn a multiple of 32")
     t, f2 = preact.shape
     if act is None:
-        act = torch.empty((t, f2 // 2), dtype=torch.bfloat16, device=dev)
+        act = preact.new_empty((t, f2 // 2))
+    else:
+        _need(act, torch.bfloat16, "act", dev, shape=(t, f2 // 2))
     if data is None:
         data = torch.empty((t, f2), dtype=torch.uint8, device=dev)
+    else:
+        _need(data, torch.uint8, "data", dev, shape=(t, f2))
     if scales is None:
-        scales = torch.empty((t, f2 // 32), dtype=torch.uint8, device=dev)
-    _need(act, torch.bfloat16, "act", dev, shape=(t, f2 // 2))
-    _need(data, torch.uint8, "data", dev, shape=(t, f2))
-    _need(scales, torch.uint8, "scales", dev, shape=(t, f2 // 32))
+        scales = data.new_empty((t, f2 // 32))
+    else:
+        _need(scales, torch.uint8, "scales", dev, shape=(t, f2 // 32))
     _launch(dev, "swiglu_mxfp8_checkpoint", preact.data_ptr(), t, f2 // 2, act.data_ptr(), data.data_ptr(),
             scales.data_ptr())
     return act, data, scales
@@ -740,11 +763,12 @@ def dswiglu_mxfp8_checkpoint(data, scales, dy, dx=None, act=None, need_act=True)
         raise ValueError("data must be [tokens, 2*ffn] with ffn a multiple of 32")
     _need(dy, torch.bfloat16, "dy", dev, shape=(t, f2 // 2))
     if dx is None:
-        dx = torch.empty((t, f2), dtype=torch.bfloat16, device=dev)
-    _need(dx, torch.bfloat16, "dx", dev, shape=(t, f2))
-    if act is None and need_act:
-        act = torch.empty((t, f2 // 2), dtype=torch.bfloat16, device=dev)
-    if act is not None:
+        dx = dy.new_empty((t, f2))
+    else:
+        _need(dx, torch.bfloat16, "dx", dev, shape=(t, f2))
+    if act is None:
+        act = dy.new_empty((t, f2 // 2)) if need_act else None
+    else:
         _need(act, torch.bfloat16, "act", dev, shape=(t, f2 // 2))
     _launch(dev, "dswiglu_mxfp8_checkpoint", data.data_ptr(), scales.data_ptr(), dy.data_ptr(), t, f2 // 2,
             dx.data_ptr(), None if act is None else act.data_ptr())
