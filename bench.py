@@ -61,7 +61,7 @@ CALLS = {
     "nvfp4_pack": (("pack.hip",), ["k_nvfp4_pack_wg (H >= 4096)", "k_nvfp4_pack"]),
     "nvfp4_pack_sr": (("pack.hip",), ["k_nvfp4_pack_sr_rows (H <= 4096)", "k_nvfp4_pack_sr"]),
     "nvfp4_pack_sr_stream": (("pack.hip",), ["k_nvfp4_pack_sr_rows (H <= 4096)", "k_nvfp4_pack_sr"]),
-    "mxfp8_pack": (("pack.hip",), ["k_mxfp8_pack"]),
+    "mxfp8_pack": (("mxfp8.h", "pack.hip"), ["k_mxfp8_pack"]),
     "nvfp4_expert_scale": (("receive.hip",), ["k_expert_scale"]),
     "nvfp4_direct_receive": (("receive.hip",), ["k_nvfp4_receive"]),
     "nvfp4_direct_receive_kblock": (("receive.hip",), ["k_nvfp4_receive (K-blocked columnwise layout)"]),
