@@ -14,7 +14,7 @@ from .binding import (  # noqa: F401
     ep_nvfp4_pack_scatter, ep_nvfp4_columnwise_grouped, ep_nvfp4_direct_receive_kblock, ep_mxfp4_direct_receive, ep_mxfp4_kblock_tile,
     ep_nvfp4_direct_receive_sr, ep_receive_workspace_bytes, ep_nvfp4_direct_receive_topk,
     dswiglu_nvfp4_quant_noalloc, EP_NOALLOC_SCRATCH_BYTES, EP_ERR_SCRATCH,
-    ep_mxfp8_unpack, ep_bf16_dispatch, ep_bf16_combine, ep_bf16_combine_bwd, ep_nvfp4_expert_matvec,
+    ep_mxfp8_unpack, ep_bf16_dispatch, ep_bf16_combine, ep_bf16_combine_bwd, ep_entry_plan, ep_nvfp4_expert_matvec,
     swiglu_mxfp8_checkpoint, dswiglu_mxfp8_checkpoint,
     lib, LIB_PATH, EXPORTS,
 )

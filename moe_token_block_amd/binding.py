@@ -623,6 +623,18 @@ def _slots(plan, dev):
     return r_cap, plan["dst_row"].shape[0], plan["dst_row"].shape[1]
 
 
+def ep_entry_plan(tokens, top_k, device):
+    """The plan under which grouped rows are the entries themselves, row t*top_k + j
+    for slot j of token t: ``ep_bf16_combine`` takes ``ep_nvfp4_expert_matvec``'s
+    output [T, k, N], viewed [T*k, N], with it.  Depends on the sizes alone; unused
+    slots need no mark in it, their rows being zero."""
+    i32 = dict(dtype=torch.int32, device=device)
+    n = tokens * top_k
+    return dict(counts=torch.full((1,), n, **i32), offsets=torch.tensor([0, n], **i32),
+                dst_row=torch.arange(n, **i32).view(tokens, top_k),
+                src_row=torch.arange(n, **i32).div(top_k, rounding_mode="floor"), r_cap=n, num_experts=1, alignment=1)
+
+
 def ep_bf16_dispatch(x, plan, out=None):
     """BF16 token rows [T, H] copied into the grouped rows of a routing plan:
     BF16 [r_cap, H], padding rows zero.  Its gradient is ``ep_bf16_combine``
