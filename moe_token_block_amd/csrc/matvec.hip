@@ -98,23 +98,31 @@ __device__ __forceinline__ void arrange(WTile& w, int kb, int K, int g) {
   w.s.y = kb + 128 * g + 64 < K ? w.s.y : 0u;
 }
 
-// The entries of expert e in order, and the rows of x they take; returns how
-// many.  Four entries a lane between barriers.
+// Four entries a lane, from `base` on (past the last: none).
 template <typename IDX>
-__device__ __forceinline__ int expert_entries(const IDX* __restrict__ ids, int M, int e, int x_div, uint16_t* list,
-                                              uint16_t* xrows, int* wcount /* [4 * waves] */) {
+__device__ __forceinline__ void load_ids(const IDX* __restrict__ ids, int M, int base, IDX* id) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int i = base + u * (int)blockDim.x + (int)threadIdx.x;
+    id[u] = i < M ? ids[i] : (IDX)-1;
+  }
+}
+
+// The entries of expert e in order, and the rows of x they take; returns how
+// many.  id: the first four of each lane, read before the first weights (loads
+// come back in order: behind the weights they would wait for them).
+template <typename IDX>
+__device__ __forceinline__ int expert_entries(const IDX* __restrict__ ids, int M, int e, int x_div, IDX* id,
+                                              uint16_t* list, uint16_t* xrows, int* wcount /* [4 * waves] */) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, B = blockDim.x, W = B >> 6;
   int n = 0;
   for (int base = 0; base < M; base += 4 * B) {
     bool hit[4];
     uint64_t m[4];
+    if (base) load_ids(ids, M, base, id);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int i = base + u * B + tid;
-      hit[u] = i < M && ids[i] == (IDX)e;
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
+      hit[u] = id[u] == (IDX)e;
       m[u] = __builtin_amdgcn_ballot_w64(hit[u]);
       if (lane == 0) wcount[u * W + wave] = __popcll(m[u]);
     }
@@ -187,7 +195,9 @@ __global__ __launch_bounds__(512) void k_nvfp4_matvec(const uint16_t* __restrict
   const int stride = WK * kStep, rounds = (K + stride - 1) / stride;  // K values of one round of the block
 
   int e = 0, n = M;
+  IDX id4[4];
   if (ids) {
+    load_ids(ids, M, 0, id4);
     e = blockIdx.y;
     if (by_entry)
       clear_unnamed(ids, tid == 0 ? e : M, M, M, E, col0, col0 + 16 * GT * WN, NO, out, d_error);
@@ -211,7 +221,7 @@ __global__ __launch_bounds__(512) void k_nvfp4_matvec(const uint16_t* __restrict
     t[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rows[i], (int)((uint32_t)r * rb + (K >> 1) + (K >> 4)), 0, 0));
   }
   if (ids) {
-    n = expert_entries(ids, M, e, x_div, list, xrows, wcount);
+    n = expert_entries(ids, M, e, x_div, id4, list, xrows, wcount);
     if (n == 0 || (by_entry && list[0] != blockIdx.y)) return;  // an earlier block has this expert
   } else {
     for (int i = tid; i < M; i += blockDim.x) list[i] = xrows[i] = (uint16_t)i;
@@ -294,10 +304,18 @@ __global__ __launch_bounds__(512) void k_nvfp4_matvec(const uint16_t* __restrict
       const int c = o & 15, v = (o >> 4) % (GT * WN), m = (o >> 4) / (GT * WN);
       const int col = col0 + 16 * v + c, i = v % GT, h = v / GT;
       if (col >= NO) continue;
+      float ys[8], us[8];  // up to eight waves' sums, read together
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int at = ((((k < WK ? k : 0) * WN + h) * RT + i) * 16 + m) * 16 + c;
+        ys[k] = red[at];
+        us[k] = SWIGLU ? red[at + GT * 256] : 0.0f;
+      }
       float y = 0.0f, u = 0.0f;
-      for (int k = 0; k < WK; ++k) {
-        y += red[(((k * WN + h) * RT + i) * 16 + m) * 16 + c];
-        if (SWIGLU) u += red[(((k * WN + h) * RT + i + GT) * 16 + m) * 16 + c];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        y += k < WK ? ys[k] : 0.0f;
+        u += k < WK ? us[k] : 0.0f;
       }
       y *= posts[(h * RT + i) * 16 + c];
       if (SWIGLU) y = y * __builtin_amdgcn_rcpf(1.0f + __expf(-y)) * (u * posts[(h * RT + i + GT) * 16 + c]);
@@ -346,7 +364,9 @@ __global__ __launch_bounds__(256, 2) void k_nvfp4_matvec_wide(const uint16_t* __
   } else {
     e = blockIdx.y;
     if (e == 0) clear_unnamed(ids, tid, 256, M, E, col0, col0 + 64 * GT, NO, out, d_error);
-    n = expert_entries(ids, M, e, x_div, list, xrows, wcount);
+    IDX id4[4];
+    load_ids(ids, M, 0, id4);
+    n = expert_entries(ids, M, e, x_div, id4, list, xrows, wcount);
     if (n == 0) return;
   }
 
