@@ -239,6 +239,22 @@ def test_dense_matvec(dev, t, n, K, swiglu):
     _check_matvec(got, expert.f64(xb), weight, None, swiglu, "dense")
 
 
+@pytest.mark.parametrize("t,e,k,swiglu", [(3, 4, 2, False), (40, 2, 2, True)])  # few and many entries an expert
+def test_matvec_at_any_address(dev, t, e, k, swiglu):
+    rng = np.random.default_rng(t)
+    weight, ids = _weights(rng, e, 50, 1088), _ids(rng, t, e, k, 0.1)
+    xb = _bits(rng.standard_normal((t, 1088)))
+    wd, xd, idd = torch.from_numpy(weight).to(dev), bf16_dev(xb, dev), torch.from_numpy(ids).to(dev)
+    base = mtb.ep_nvfp4_expert_matvec(xd, wd, idd, swiglu=swiglu)
+    _check_matvec(base, expert.f64(xb), weight, ids, swiglu, "aligned")
+    for off in (1, 2, 3, 7):
+        wo = torch.empty(wd.numel() + 8, dtype=torch.uint8, device=dev)[off : off + wd.numel()].view(wd.shape)
+        xo = torch.empty(xd.numel() + 8, dtype=torch.bfloat16, device=dev)[off : off + xd.numel()].view(xd.shape)
+        wo.copy_(wd)
+        xo.copy_(xd)
+        assert_bytes_equal(host(mtb.ep_nvfp4_expert_matvec(xo, wo, idd, swiglu=swiglu)), host(base), f"offset {off}")
+
+
 def test_matvec_drops_and_flags_bad_ids(dev):
     rng = np.random.default_rng(11)
     weight = _weights(rng, 3, 20, 128)
