@@ -108,25 +108,43 @@ def _stream(dev):
     return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
 
 
-# The current stream's handle without a Stream object around it: 0.1 us of a
-# call's host time instead of 1.9 (a single token's call is bound by the host).
+# The calls of the expert layer serve single tokens too, where the host's time is
+# the call's: the current device and stream are read without an object around
+# them (0.1 us instead of 0.3 and 1.9), and tensors are checked in one expression.
+_BF16, _F32, _I32T, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _launch(dev, name, *args):
-    """Calls entry point ``name`` on ``dev`` and its current stream; addresses are
-    plain integers (None: NULL).  The device is switched only when another one is
-    current."""
+def _launch(index, name, *args):
+    """Calls entry point ``name`` on device ``index`` and its current stream;
+    addresses are plain integers (None: NULL).  The device is switched only when
+    another one is current."""
     f = getattr(_lib or lib(), name)
-    index = dev.index
-    if torch.cuda.current_device() == index:
+    if _raw_device() == index:
         status = f(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             status = f(*args, _raw_stream(index))
     if status:
         _check(status, name)
+
+
+def _index(t):
+    """The GPU that holds ``t``."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("tensors must live on a GPU (no CPU path)")
+    return index
+
+
+def _want(t, dtype, name, index, shape):
+    """Refuses (as ``_need``) a tensor that is not a contiguous ``dtype`` one of
+    ``shape`` on GPU ``index``."""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and t.is_contiguous()):
+        _need(t, dtype, name, torch.device("cuda", index), shape=shape)
 
 
 def _dev(t):
@@ -140,9 +158,6 @@ def _need(t, dtype, name, dev=None, shape=None, numel=None):
     size -- an exact ``shape``, or at least ``numel`` elements.  The C ABI gets
     raw pointers, so this is the only place a buffer too small for the sizes
     passed with it can be caught before a kernel writes past its end."""
-    if (type(t) is torch.Tensor and t.dtype is dtype and numel is None and (shape is None or t.shape == shape)
-            and (dev is None or t.device == dev) and t.is_contiguous()):
-        return  # all in order, in one go: several of these are made for every call
     if not torch.is_tensor(t):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype != dtype:
@@ -285,25 +300,26 @@ def ep_mxfp8_pack(x, out=None):
     return data, scales, out
 
 
-def _mxfp8(data, scales):
-    """Device and sizes of MXFP8 rows: data [rows, hidden], scales [rows, hidden/32]."""
-    dev = _dev(data)
-    _need(data, torch.uint8, "data")
-    if data.dim() != 2 or data.shape[1] % 32:
-        raise ValueError("data must be [rows, hidden] with hidden a multiple of 32")
-    rows, hidden = data.shape
-    _need(scales, torch.uint8, "scales", dev, shape=(rows, hidden // 32))
-    return dev, rows, hidden
+def _mxfp8(data, scales, block):
+    """GPU and sizes of MXFP8 rows: data [rows, width] with width a multiple of
+    ``block``, scales [rows, width/32]."""
+    index = _index(data)
+    if data.dim() != 2 or data.shape[1] % block:
+        raise ValueError(f"data must be [rows, width] with width a multiple of {block}")
+    rows, width = data.shape
+    _want(data, _U8, "data", index, (rows, width))
+    _want(scales, _U8, "scales", index, (rows, width // 32))
+    return index, rows, width
 
 
 def ep_mxfp8_unpack(data, scales, out=None):
     """MXFP8 rows (data uint8 [T, H], scales uint8 [T, H/32]) -> BF16 [T, H]."""
-    dev, t, h = _mxfp8(data, scales)
+    index, t, h = _mxfp8(data, scales, 32)
     if out is None:
-        out = torch.empty((t, h), dtype=torch.bfloat16, device=dev)
+        out = data.new_empty((t, h), dtype=_BF16)
     else:
-        _need(out, torch.bfloat16, "out", dev, shape=(t, h))
-    _launch(dev, "ep_mxfp8_unpack", data.data_ptr(), scales.data_ptr(), t, h, out.data_ptr())
+        _want(out, _BF16, "out", index, (t, h))
+    _launch(index, "ep_mxfp8_unpack", data.data_ptr(), scales.data_ptr(), t, h, out.data_ptr())
     return out
 
 
@@ -605,22 +621,23 @@ def ep_mxfp8_direct_receive(data, scales, plan, out=None):
 
 
 # ------------------------------------------------------------------ BF16 dispatch / combine
-def _rows(t, name, rows=None, hidden=None, dev=None):
-    """A BF16 matrix of rows, with the sizes given."""
-    _need(t, torch.bfloat16, name, dev)
-    if t.shape == (rows, hidden):
-        return
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (hidden is not None and t.shape[1] != hidden):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{'rows' if rows is None else rows}, "
-                         f"{'hidden' if hidden is None else hidden}]")
-
-
-def _slots(plan, dev):
-    """Sizes of a plan whose maps both ways are used: r_cap, tokens, top_k."""
-    _, r_cap = _plan(plan, dev)
-    if plan["dst_row"].dim() != 2:
+def _slots(plan, index, src=False):
+    """r_cap, tokens and top_k of a plan, its maps that a call hands over checked:
+    dst_row, and with ``src`` src_row."""
+    r_cap, d = int(plan["r_cap"]), plan["dst_row"]
+    if d.dim() != 2:
         raise ValueError("plan dst_row must be [tokens, top_k]")
-    return r_cap, plan["dst_row"].shape[0], plan["dst_row"].shape[1]
+    t, k = d.shape
+    _want(d, _I32T, "plan dst_row", index, (t, k))
+    if src:
+        _want(plan["src_row"], _I32T, "plan src_row", index, (r_cap,))
+    return r_cap, t, k
+
+
+def _width(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, hidden]")
+    return t.shape[1]
 
 
 def ep_entry_plan(tokens, top_k, device):
@@ -639,15 +656,14 @@ def ep_bf16_dispatch(x, plan, out=None):
     """BF16 token rows [T, H] copied into the grouped rows of a routing plan:
     BF16 [r_cap, H], padding rows zero.  Its gradient is ``ep_bf16_combine``
     without weights."""
-    dev = _dev(x)
-    r_cap, t, k = _slots(plan, dev)
-    _rows(x, "x", rows=t)
-    h = x.shape[1]
+    index, h = _index(x), _width(x, "x")
+    r_cap, t, k = _slots(plan, index, src=True)
+    _want(x, _BF16, "x", index, (t, h))
     if out is None:
         out = x.new_empty((r_cap, h))
     else:
-        _rows(out, "out", r_cap, h, dev)
-    _launch(dev, "ep_bf16_dispatch", x.data_ptr(), t, h, k, r_cap, plan["dst_row"].data_ptr(),
+        _want(out, _BF16, "out", index, (r_cap, h))
+    _launch(index, "ep_bf16_dispatch", x.data_ptr(), t, h, k, r_cap, plan["dst_row"].data_ptr(),
             plan["src_row"].data_ptr(), out.data_ptr())
     return out
 
@@ -657,17 +673,16 @@ def ep_bf16_combine(rows, plan, weights=None, out=None):
     of weights[t, j] * rows[dst_row[t, j]] (FP32 sum, BF16 [T, H]); ``weights``
     float32 [T, k], or None for a plain sum (the gradient of ``ep_bf16_dispatch``).
     Unused slots add nothing; padding rows are not read."""
-    dev = _dev(rows)
-    r_cap, t, k = _slots(plan, dev)
-    _rows(rows, "rows", rows=r_cap)
-    h = rows.shape[1]
+    index, h = _index(rows), _width(rows, "rows")
+    r_cap, t, k = _slots(plan, index)
+    _want(rows, _BF16, "rows", index, (r_cap, h))
     if weights is not None:
-        _need(weights, torch.float32, "weights", dev, shape=(t, k))
+        _want(weights, _F32, "weights", index, (t, k))
     if out is None:
         out = rows.new_empty((t, h))
     else:
-        _rows(out, "out", t, h, dev)
-    _launch(dev, "ep_bf16_combine", rows.data_ptr(), r_cap, h, t, k, plan["dst_row"].data_ptr(),
+        _want(out, _BF16, "out", index, (t, h))
+    _launch(index, "ep_bf16_combine", rows.data_ptr(), r_cap, h, t, k, plan["dst_row"].data_ptr(),
             None if weights is None else weights.data_ptr(), out.data_ptr())
     return out
 
@@ -675,22 +690,22 @@ def ep_bf16_combine(rows, plan, weights=None, out=None):
 def ep_bf16_combine_bwd(dout, rows, plan, weights, drows=None, dweights=None):
     """Gradients of ``ep_bf16_combine`` for dout BF16 [T, H]: (drows BF16 [r_cap, H],
     padding rows zero; dweights float32 [T, k], 0 for unused slots)."""
-    dev = _dev(dout)
-    r_cap, t, k = _slots(plan, dev)
-    _rows(dout, "dout", rows=t)
-    h = dout.shape[1]
-    _rows(rows, "rows", r_cap, h, dev)
-    _need(weights, torch.float32, "weights", dev, shape=(t, k))
+    index, h = _index(dout), _width(dout, "dout")
+    r_cap, t, k = _slots(plan, index, src=True)
+    _want(dout, _BF16, "dout", index, (t, h))
+    _want(rows, _BF16, "rows", index, (r_cap, h))
+    _want(weights, _F32, "weights", index, (t, k))
     if drows is None:
         drows = rows.new_empty((r_cap, h))
     else:
-        _rows(drows, "drows", r_cap, h, dev)
+        _want(drows, _BF16, "drows", index, (r_cap, h))
     if dweights is None:
         dweights = weights.new_empty((t, k))
     else:
-        _need(dweights, torch.float32, "dweights", dev, shape=(t, k))
-    _launch(dev, "ep_bf16_combine_bwd", dout.data_ptr(), rows.data_ptr(), t, h, k, r_cap, plan["dst_row"].data_ptr(),
-            plan["src_row"].data_ptr(), weights.data_ptr(), drows.data_ptr(), dweights.data_ptr())
+        _want(dweights, _F32, "dweights", index, (t, k))
+    _launch(index, "ep_bf16_combine_bwd", dout.data_ptr(), rows.data_ptr(), t, h, k, r_cap,
+            plan["dst_row"].data_ptr(), plan["src_row"].data_ptr(), weights.data_ptr(), drows.data_ptr(),
+            dweights.data_ptr())
     return drows, dweights
 
 
@@ -706,36 +721,37 @@ def ep_nvfp4_expert_matvec(x, weight, topk_idx=None, swiglu=False, out=None, d_e
     the result is silu(gate) * up, [T, k, N/2].  Without ``topk_idx``, ``weight`` is
     one matrix [N, 9K/16 + 4] and the result [T, N] (or [T, N/2]).  ``d_error``:
     optional device int32 [1], OR-ed with EP_DEVERR_EXPERT_ID on a bad id."""
-    dev = _dev(x)
-    _need(x, torch.bfloat16, "x")
-    _need(weight, torch.uint8, "weight", dev)
-    dense = topk_idx is None
-    if x.dim() not in ((2,) if dense else (2, 3)):
+    index, dense = _index(x), topk_idx is None
+    if x.dim() != 2 and (dense or x.dim() != 3):
         raise ValueError("x must be [tokens, hidden]" + ("" if dense else " or [tokens, top_k, hidden]"))
     t, h = x.shape[0], x.shape[-1]
-    rb = 9 * (h // 16) + 4 if h % 64 == 0 and h > 0 else _row_bytes(h, "ep_nvfp4_expert_matvec")
+    _want(x, _BF16, "x", index, x.shape)
+    rb = 9 * (h // 16) + 4 if h > 0 and h % 64 == 0 else _row_bytes(h, "ep_nvfp4_expert_matvec")
     if weight.dim() != (2 if dense else 3) or weight.shape[-1] != rb:
         raise ValueError(f"weight has shape {tuple(weight.shape)}, expected [{'' if dense else 'experts, '}width, {rb}] "
                          f"for hidden {h}")
+    _want(weight, _U8, "weight", index, weight.shape)
     e, n = (1 if dense else weight.shape[0]), weight.shape[-2]
     if swiglu and n % 2:
         raise ValueError("swiglu needs an even number of weight rows ([gate | up])")
+    width = n // 2 if swiglu else n
     k, idt, ids = 1, EP_IDX_INT32, None
-    if not dense:
+    if dense:
+        shape = (t, width)
+    else:
         idt = _topk(topk_idx)
         k, ids = topk_idx.shape[1], topk_idx.data_ptr()
-        if topk_idx.device != dev or topk_idx.shape[0] != t or (x.dim() == 3 and x.shape[1] != k):
-            raise ValueError(f"topk_idx must be [tokens, top_k] on {dev}, as x {tuple(x.shape)} has them")
-    width = n // 2 if swiglu else n
-    shape = (t, width) if dense else (t, k, width)
+        if topk_idx.get_device() != index or topk_idx.shape[0] != t or (x.dim() == 3 and x.shape[1] != k):
+            raise ValueError(f"topk_idx must be [tokens, top_k] on x's GPU, as x {tuple(x.shape)} has them")
+        shape = (t, k, width)
     if out is None:
         out = x.new_empty(shape)
     else:
-        _need(out, torch.bfloat16, "out", dev, shape=shape)
+        _want(out, _BF16, "out", index, shape)
     if d_error is not None:
-        _need(d_error, torch.int32, "d_error", dev, numel=1)
-    _launch(dev, "ep_nvfp4_expert_matvec", x.data_ptr(), t, h, int(x.dim() == 3), weight.data_ptr(), e, n, ids, idt, k,
-            int(swiglu), out.data_ptr(), None if d_error is None else d_error.data_ptr())
+        _need(d_error, torch.int32, "d_error", x.device, numel=1)
+    _launch(index, "ep_nvfp4_expert_matvec", x.data_ptr(), t, h, int(x.dim() == 3), weight.data_ptr(), e, n, ids, idt,
+            k, int(swiglu), out.data_ptr(), None if d_error is None else d_error.data_ptr())
     return out
 
 
@@ -744,24 +760,24 @@ def swiglu_mxfp8_checkpoint(preact, act=None, data=None, scales=None):
     """act = silu(a) * b of BF16 preact [T, 2F] = [a | b], and preact kept as MXFP8
     (the bytes of ``ep_mxfp8_pack``): (act BF16 [T, F], data uint8 [T, 2F], scales
     uint8 [T, 2F/32])."""
-    dev = _dev(preact)
-    _need(preact, torch.bfloat16, "preact")
+    index = _index(preact)
     if preact.dim() != 2 or preact.shape[1] % 64:
         raise ValueError("preact must be [tokens, 2*ffn] with ffn a multiple of 32")
     t, f2 = preact.shape
+    _want(preact, _BF16, "preact", index, (t, f2))
     if act is None:
         act = preact.new_empty((t, f2 // 2))
     else:
-        _need(act, torch.bfloat16, "act", dev, shape=(t, f2 // 2))
+        _want(act, _BF16, "act", index, (t, f2 // 2))
     if data is None:
-        data = torch.empty((t, f2), dtype=torch.uint8, device=dev)
+        data = preact.new_empty((t, f2), dtype=_U8)
     else:
-        _need(data, torch.uint8, "data", dev, shape=(t, f2))
+        _want(data, _U8, "data", index, (t, f2))
     if scales is None:
         scales = data.new_empty((t, f2 // 32))
     else:
-        _need(scales, torch.uint8, "scales", dev, shape=(t, f2 // 32))
-    _launch(dev, "swiglu_mxfp8_checkpoint", preact.data_ptr(), t, f2 // 2, act.data_ptr(), data.data_ptr(),
+        _want(scales, _U8, "scales", index, (t, f2 // 32))
+    _launch(index, "swiglu_mxfp8_checkpoint", preact.data_ptr(), t, f2 // 2, act.data_ptr(), data.data_ptr(),
             scales.data_ptr())
     return act, data, scales
 
@@ -770,19 +786,17 @@ def dswiglu_mxfp8_checkpoint(data, scales, dy, dx=None, act=None, need_act=True)
     """The gradient of SwiGLU from its 8-bit checkpoint: (dx BF16 [T, 2F] = [da | db],
     act BF16 [T, F] computed again from the checkpoint, or None with
     ``need_act=False``)."""
-    dev, t, f2 = _mxfp8(data, scales)
-    if f2 % 64:
-        raise ValueError("data must be [tokens, 2*ffn] with ffn a multiple of 32")
-    _need(dy, torch.bfloat16, "dy", dev, shape=(t, f2 // 2))
+    index, t, f2 = _mxfp8(data, scales, 64)
+    _want(dy, _BF16, "dy", index, (t, f2 // 2))
     if dx is None:
         dx = dy.new_empty((t, f2))
     else:
-        _need(dx, torch.bfloat16, "dx", dev, shape=(t, f2))
+        _want(dx, _BF16, "dx", index, (t, f2))
     if act is None:
         act = dy.new_empty((t, f2 // 2)) if need_act else None
     else:
-        _need(act, torch.bfloat16, "act", dev, shape=(t, f2 // 2))
-    _launch(dev, "dswiglu_mxfp8_checkpoint", data.data_ptr(), scales.data_ptr(), dy.data_ptr(), t, f2 // 2,
+        _want(act, _BF16, "act", index, (t, f2 // 2))
+    _launch(index, "dswiglu_mxfp8_checkpoint", data.data_ptr(), scales.data_ptr(), dy.data_ptr(), t, f2 // 2,
             dx.data_ptr(), None if act is None else act.data_ptr())
     return dx, act
 
