@@ -158,16 +158,17 @@ __device__ __forceinline__ void clear_unnamed(const IDX* __restrict__ ids, int i
   }
 }
 
-// Few entries per expert.  One block per expert (by_entry: per entry, and the
-// first with an expert takes all of that expert's) and WN * RT tiles of 16 weight
+// Few entries per expert, or few blocks.  One block per expert (by_entry: per
+// entry, and the first with an expert takes all of that expert's; or several that
+// take the expert's entries 16 at a time in turn) and WN * RT tiles of 16 weight
 // rows.  WN waves side by side have RT tiles each; WK waves deep take the K steps
 // in turn, and their sums are joined through LDS.  16 entries are taken in one
 // pass over the weights; their activations come through LDS, kc columns at a time
 // (a power of two, whole rounds of the WK waves), rows padded by 16 bytes so that
 // the 16 entries of a read lie in different banks.
 //
-// 8 tokens, top-8 of 32 experts, 7168 x 2048: 61 us for 232 MB (3.8 TB/s); one
-// token, top-8 of 32, 4096 x 7168 with SwiGLU: 33 us for 132 MB (4.0 TB/s); the
+// 8 tokens, top-8 of 32 experts, 7168 x 2048: 59 us for 232 MB (3.9 TB/s); one
+// token, top-8 of 32, 4096 x 7168 with SwiGLU: 30 us for 132 MB (4.4 TB/s); the
 // same weights by a wave per output and entry: 133 us for the first.  What is left
 // above the copy rate is a block's first loads, which the few blocks of such a
 // call do not hide, and lines fetched twice: rows of 9 K / 16 + 4 bytes end
@@ -236,9 +237,10 @@ __global__ __launch_bounds__(512) void k_nvfp4_matvec(const uint16_t* __restrict
     t[i] = t[i] < 0x1p-64f ? t[i] * 0x1p64f : t[i];
   }
 
-  for (int c0 = 0; c0 < n; c0 += 16) {
+  const int first = 16 * (int)blockIdx.z;
+  for (int c0 = first; c0 < n; c0 += 16 * (int)gridDim.z) {
     const int cols = min(n - c0, 16);
-    if (c0) {
+    if (c0 != first) {
 #pragma unroll
       for (int i = 0; i < RT; ++i) load_tile(rows[i], code, scale, rb, wk * kStep, w[i]);
     }
@@ -277,6 +279,11 @@ __global__ __launch_bounds__(512) void k_nvfp4_matvec(const uint16_t* __restrict
       const uint16_t* xl = xs + min(r, cols - 1) * xrow + (kb & (kc - 1)) + 128 * g;
 #pragma unroll
       for (int i = 0; i < RT; ++i) arrange(w[i], kb, K, g);
+      // a wave that has its weights goes first, so that those of a CU fall out of
+      // step and one's loads meet another's products (64 entries of 7168 x 7168:
+      // 33 -> 28 us; 4096 x 7168 of 32 experts, 16 tokens: 120 -> 116; where each SIMD
+      // has the waves of one deep block, which wait for each other anyway: -1%)
+      if (WN == 2) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int j = 0; j < 16; ++j) {  // word j % 4 of chunk j / 4
         const bf16x8 b = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(xl + 8 * j));
@@ -285,6 +292,7 @@ __global__ __launch_bounds__(512) void k_nvfp4_matvec(const uint16_t* __restrict
           acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
               decode8(w[i].c[j >> 2][j & 3], block_scale(j < 8 ? w[i].s.x : w[i].s.y, (j >> 1) & 3), t[i]), b, acc[i], 0, 0, 0);
       }
+      if (WN == 2) __builtin_amdgcn_s_setprio(0);
       if (kb + stride < K) {
 #pragma unroll
         for (int i = 0; i < RT; ++i) load_tile(rows[i], code, scale, rb, kb + stride, w[i]);
@@ -512,12 +520,14 @@ MTB_EXPORT int32_t ep_nvfp4_expert_matvec(const uint16_t* x, int64_t tokens, int
   hipStream_t s = (hipStream_t)stream;
   const int NO = swiglu ? N / 2 : N;
   constexpr int RT = 2;
-  // From 8 entries an expert on, the wide kernel (8: 150 us against 192 at 64 tokens,
-  // top-8 of 32, 4096 x 7168; 4, at 16 tokens: 139 against 121).
-  if (M >= 8 * E) {
-        constexpr int NT = 4;
-    const int cols = (swiglu ? 32 : 64) * RT;
-    const dim3 grid((unsigned)((NO + cols - 1) / cols), (unsigned)E);
+  // From 16 entries an expert on, the wide kernel, if its blocks reach every CU.
+  // 4096 x 7168 with SwiGLU, 32 experts: 16 entries each 144 us against 190; 12:
+  // 145, 141; 8: 140, 126; 7168 x 2048: 12: 85, 80; 8: 83, 71.  128 entries of one
+  // 7168 x 7168 matrix would be 56 of its blocks and 119 us, against 47.
+  const int wide_cols = (swiglu ? 32 : 64) * RT, wide_blocks = (NO + wide_cols - 1) / wide_cols * E;
+  if (M >= 16 * E && wide_blocks >= 256) {
+    constexpr int NT = 4;
+    const dim3 grid((unsigned)(wide_blocks / E), (unsigned)E);
     const size_t lds = (size_t)NT * 16 * 264 * 2 * 2 + 4 * (size_t)M;
 #define MTB_WIDE(SW, IDX)                                                                                      \
   hipLaunchKernelGGL((k_nvfp4_matvec_wide<RT, NT, SW, IDX>), grid, dim3(256), lds, s, x, K, x_div, weight, E, N, \
@@ -533,20 +543,28 @@ MTB_EXPORT int32_t ep_nvfp4_expert_matvec(const uint16_t* x, int64_t tokens, int
     return launch_status();
   }
   const int slots = topk_idx ? (by_entry ? M : E) : 1, mc = min(M, 16);  // mc: entries of one pass
-  // Blocks of 2 x 2 waves, unless those would not reach every CU: then each block
-  // has half the rows, and up to eight waves share out its K steps (within 64 KB
-  // of LDS).  One token, 2 of 8 experts, 4096 x 4096: 11.5 us against 13.3; 8
-  // tokens, top-8 of 32, 7168 x 2048: 99 against 62.
+  // Blocks of 2 x 2 waves.  Where those would not reach every CU, an expert's
+  // entries are shared out too, 16 a block (up to twice the mean; a block takes the
+  // rest in turn).  Where that is not enough either, a block has half the rows,
+  // and up to eight waves share out its K steps, as its share of the CU's LDS
+  // allows.  7168 x 7168 times 64 entries: 28 us, with half rows 53, by few wide
+  // blocks 61; 16 entries: 15 with half rows, 38 by few wide blocks; one
+  // token, 2 of 8 experts, 4096 x 4096: 9.8 against 13.2 by whole rows; 8 tokens,
+  // top-8 of 32, 7168 x 2048: 70 and 60.
   const int cols2 = (swiglu ? 16 : 32) * RT;
-  const bool few = (int64_t)((NO + cols2 - 1) / cols2) * slots < 256;
-  const int WN = few ? 1 : 2, most = few ? 8 : 2;
+  const int64_t blocks2 = (int64_t)((NO + cols2 - 1) / cols2) * slots;
+  const int parts = by_entry || blocks2 >= 256 ? 1 : min((M + 15) / 16, (2 * M + 16 * E - 1) / (16 * E));
+  const bool few = blocks2 * parts < 256;
+  const int WN = few ? 1 : 2, most = few ? 8 : 2, cols = (swiglu ? 8 : 16) * RT * WN;
+  const dim3 grid((unsigned)((NO + cols - 1) / cols), (unsigned)slots, (unsigned)parts);
+  // one block a CU, or two (32 entries of 7168 x 7168: 22 us, 28 by one at a time)
+  const size_t room = (few && grid.x * grid.y * grid.z <= 256 ? 140 : 70) << 10;
   int WK = 1;
-  while (2 * WK <= most && WK * kStep < K && mc * (2 * WK * kStep + 8) * 2 <= (60 << 10)) WK *= 2;
-  const int cols = (swiglu ? 8 : 16) * RT * WN;
+  while (2 * WK <= most && WK * kStep < K && (size_t)mc * (2 * WK * kStep + 8) * 2 <= room) WK *= 2;
   size_t lds_x = max((size_t)mc * (WK * kStep + 8) * 2, (size_t)WK * WN * RT * 1024 + WN * RT * 64);
   lds_x = max(lds_x, min((size_t)mc * (4 * (size_t)K + 16), (size_t)32 << 10));
   lds_x = (lds_x + 15) & ~(size_t)15;
-  const dim3 grid((unsigned)((NO + cols - 1) / cols), (unsigned)slots), block(64 * WK * WN);
+  const dim3 block(64 * WK * WN);
   const size_t lds = lds_x + 4 * (size_t)M;
 #define MTB_MATVEC(WN, SW, IDX)                                                                                 \
   hipLaunchKernelGGL((k_nvfp4_matvec<RT, WN, SW, IDX>), grid, block, lds, s, x, K, x_div, weight, E, N,         \

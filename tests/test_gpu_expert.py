@@ -228,6 +228,37 @@ def test_expert_matvec(dev, case):
     assert_bytes_equal(host(again), host(got), "the same call with 64-bit ids")
 
 
+# Entries of each expert (and of none), width, hidden, swiglu.  First widths at which four waves side by side
+# fill the GPU: passes of one to four column tiles, more than one pass, an empty expert; then few rows of
+# weights, whose entries several blocks share out, some in more than one turn.
+SHARES = [([1, 17, 33, 49, 64, 65, 150, 0, 16, 2, 3, 48, 5, 6, 32, 7], 9, 2050, 576, False),
+          ([1, 17, 33, 49, 64, 65, 150, 0, 16, 2, 3, 48, 5, 6, 32, 7], 0, 2050, 1088, True),
+          ([130, 70, 31, 1, 16, 17, 0, 8], 3, 4030, 64, False),
+          ([200, 0, 40], 5, 40, 7168, False), ([200, 1, 39], 0, 42, 1600, True),
+          ([230, 0, 10], 2, 1300, 1088, False), ([16, 300, 33], 0, 700, 2112, True), ([40, 4000], 30, 3, 128, False)]
+
+
+@pytest.mark.parametrize("case", SHARES)
+def test_matvec_with_uneven_experts(dev, case):
+    counts, none, n, K, swiglu = case
+    rng = np.random.default_rng(n + K)
+    ids = np.repeat(np.arange(-1, len(counts)), [none] + counts).astype(np.int32)
+    rng.shuffle(ids)
+    ids = ids[:, None]
+    weight = _weights(rng, len(counts), n, K)
+    xb = _bits(rng.standard_normal((ids.size, K)))
+    print(f"matvec {case}", flush=True)
+    xd, wd, idd = bf16_dev(xb, dev), torch.from_numpy(weight).to(dev), torch.from_numpy(ids).to(dev)
+    got = mtb.ep_nvfp4_expert_matvec(xd, wd, idd, swiglu=swiglu)
+    _check_matvec(got, expert.f64(xb), weight, ids, swiglu, f"matvec {case}")
+    assert not host(got)[ids < 0].any()
+    wo = torch.empty(wd.numel() + 8, dtype=torch.uint8, device=dev)[3 : 3 + wd.numel()].view(wd.shape)
+    xo = torch.empty(xd.numel() + 8, dtype=torch.bfloat16, device=dev)[1 : 1 + xd.numel()].view(xd.shape)
+    wo.copy_(wd)
+    xo.copy_(xd)
+    assert_bytes_equal(host(mtb.ep_nvfp4_expert_matvec(xo, wo, idd.long(), swiglu=swiglu)), host(got), "odd addresses")
+
+
 @pytest.mark.parametrize("t,n,K,swiglu", [(1, 1, 64, False), (1, 4096, 128, True), (3, 1001, 1088, False),
                                           (20, 77, 960, False), (130, 34, 192, True), (2, 16, 16384, False)])
 def test_dense_matvec(dev, t, n, K, swiglu):
