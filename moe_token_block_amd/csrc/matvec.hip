@@ -441,16 +441,23 @@ __global__ __launch_bounds__(256, 2) void k_nvfp4_matvec_wide(const uint16_t* __
         }
       }
     };
+    // With three tiles or four the products take longest, and a wave that has its
+    // operands goes first (7168 x 2048, 128 tokens, top-8 of 32: 102 -> 97 us; with one
+    // or two, which wait for weights most: 144 -> 153 us at 64 tokens of 4096 x 7168).
     auto step = [&](int kb, WTile* w, WTile* next) {
       load_x(kb + 64);
       if (kb + kStep < K) load_w(kb + kStep, next);
 #pragma unroll
       for (int i = 0; i < RT; ++i) arrange(w[i], kb, K, g);
+      if (NA >= 3) __builtin_amdgcn_s_setprio(1);
       half(0, w);
+      if (NA >= 3) __builtin_amdgcn_s_setprio(0);
       store_x(1, kb + 64);
       __syncthreads();
       load_x(kb + kStep);
+      if (NA >= 3) __builtin_amdgcn_s_setprio(1);
       half(1, w);
+      if (NA >= 3) __builtin_amdgcn_s_setprio(0);
       store_x(0, kb + kStep);
       __syncthreads();
     };
