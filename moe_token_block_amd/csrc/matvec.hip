@@ -167,7 +167,7 @@ __device__ __forceinline__ void clear_unnamed(const IDX* __restrict__ ids, int i
 // (a power of two, whole rounds of the WK waves), rows padded by 16 bytes so that
 // the 16 entries of a read lie in different banks.
 //
-// 8 tokens, top-8 of 32 experts, 7168 x 2048: 59 us for 232 MB (3.9 TB/s); one
+// 8 tokens, top-8 of 32 experts, 7168 x 2048: 60 us for 232 MB (3.9 TB/s); one
 // token, top-8 of 32, 4096 x 7168 with SwiGLU: 30 us for 132 MB (4.4 TB/s); the
 // same weights by a wave per output and entry: 133 us for the first.  What is left
 // above the copy rate is a block's first loads, which the few blocks of such a
@@ -341,8 +341,8 @@ __global__ __launch_bounds__(512) void k_nvfp4_matvec(const uint16_t* __restrict
 // way in registers, and so are the next step's weights, issued after it, so that
 // neither wait includes the other.
 //
-// 128 tokens, top-8 of 32, 4096 x 7168 with SwiGLU: 175 us, 3.1 TB/s of weights
-// and 344 TFLOP/s; passes of 16 entries, which read the weights again for every
+// 128 tokens, top-8 of 32, 4096 x 7168 with SwiGLU: 172 us, 3.1 TB/s of weights
+// and 349 TFLOP/s; passes of 16 entries, which read the weights again for every
 // 16, take 309.  Alone, the reads take 89 us and the decoding and products 104:
 // the two waves of a SIMD, in step with their blocks' barriers, overlap them only
 // in part.  Measured without gain: weights two and three steps ahead (they share
