@@ -535,7 +535,8 @@ int32_t ep_bf16_combine_bwd(const uint16_t* dout, const uint16_t* rows, int64_t 
  * sets EP_DEVERR_EXPERT_ID in *d_error (d_error may be NULL).  No row of x that
  * only such entries name is read.
  *   topk_idx [tokens, top_k] int32 or int64 (idx_dtype); NULL: one dense matrix
- *   (num_experts and top_k 1).  out [tokens, top_k, width or width/2] BF16.
+ *   (num_experts and top_k 1; with no tokens any, as an empty map's address may
+ *   be NULL).  out [tokens, top_k, width or width/2] BF16.
  *   Requires hidden a positive multiple of 64, at most 2^20; 1 <= num_experts
  *   <= 1024; 1 <= width <= 2^24, even with swiglu; tokens * top_k <= 4096
  *   (EP_ERR_RANGE: larger batches are a matrix product's). */

@@ -516,11 +516,11 @@ MTB_EXPORT int32_t ep_nvfp4_expert_matvec(const uint16_t* x, int64_t tokens, int
   if (tokens < 0 || hidden <= 0 || hidden % 64 != 0 || num_experts < 1 || num_experts > 1024 || width < 1 ||
       top_k < 1 || (swiglu && width % 2 != 0))
     return EP_ERR_SHAPE;
-  if (!topk_idx && (num_experts != 1 || top_k != 1)) return EP_ERR_SHAPE;
   if (idx_dtype != EP_IDX_INT32 && idx_dtype != EP_IDX_INT64) return EP_ERR_DTYPE;
   if (tokens >= kSizeLimit || top_k > 1024 || hidden > (1 << 20) || width > (1 << 24) || tokens * top_k > kMaxEntries)
     return EP_ERR_RANGE;
-  if (tokens == 0) return EP_OK;
+  if (tokens == 0) return EP_OK;  // before topk_idx is looked at: an empty tensor's address may be NULL
+  if (!topk_idx && (num_experts != 1 || top_k != 1)) return EP_ERR_SHAPE;
   if (!x || !weight || !out) return EP_ERR_NULL;
   const int M = (int)(tokens * top_k), E = (int)num_experts, N = (int)width, K = (int)hidden;
   const int by_entry = topk_idx && M < E, x_div = x_per_entry ? 1 : (int)top_k;  // entry -> row of x
