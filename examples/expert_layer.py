@@ -80,7 +80,7 @@ def serve(x, topk_idx, weights, packed, entries):
     w1, w2 = packed
     act = m.ep_nvfp4_expert_matvec(x, w1, topk_idx, swiglu=True)
     y = m.ep_nvfp4_expert_matvec(act, w2, topk_idx)
-    return m.ep_bf16_combine(y.view(-1, y.shape[2]), entries, weights)
+    return m.ep_bf16_combine(y.view(-1, y.shape[2]), entries, weights, topk_idx=topk_idx, num_experts=w2.shape[0])
 
 
 def main():

@@ -506,6 +506,16 @@ int32_t ep_bf16_dispatch(const uint16_t* x, int64_t tokens, int64_t hidden, int6
 int32_t ep_bf16_combine(const uint16_t* rows, int64_t r_cap, int64_t hidden, int64_t tokens, int64_t top_k,
                         const int32_t* dst_row, const float* weights, uint16_t* out, void* stream);
 
+/* ep_bf16_combine_topk: ep_bf16_combine where the slots whose topk_idx lies
+ * outside [0, num_experts) add nothing either (neither their weight nor their
+ * row is used), for maps that do not mark them: a map made once for a number of
+ * tokens, whose rows are the entries of ep_nvfp4_expert_matvec.
+ *   topk_idx [tokens, top_k] int32 or int64 (idx_dtype), 1 <= num_experts <= 1024;
+ *   the others as for ep_bf16_combine. */
+int32_t ep_bf16_combine_topk(const uint16_t* rows, int64_t r_cap, int64_t hidden, int64_t tokens, int64_t top_k,
+                             const int32_t* dst_row, const void* topk_idx, int32_t idx_dtype, int64_t num_experts,
+                             const float* weights, uint16_t* out, void* stream);
+
 /* ep_bf16_combine_bwd: the gradients of ep_bf16_combine,
  *   drows[dst_row[t, j]] = weights[t, j] * dout[t]          (BF16, one rounding)
  *   dweights[t, j] = sum over h of dout[t, h] * rows[dst_row[t, j], h]  (FP32)

@@ -61,6 +61,7 @@ _SIGS = {
     "ep_mxfp8_unpack": (_I32, [_P, _P, _I64, _I64, _P, _P]),
     "ep_bf16_dispatch": (_I32, [_P, _I64, _I64, _I64, _I64, _P, _P, _P, _P]),
     "ep_bf16_combine": (_I32, [_P, _I64, _I64, _I64, _I64, _P, _P, _P, _P]),
+    "ep_bf16_combine_topk": (_I32, [_P, _I64, _I64, _I64, _I64, _P, _P, _I32, _I64, _P, _P, _P]),
     "ep_bf16_combine_bwd": (_I32, [_P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P]),
     "ep_nvfp4_expert_matvec": (_I32, [_P, _I64, _I64, _I32, _P, _I64, _I64, _P, _I32, _I64, _I32, _P, _P, _P]),
     "swiglu_mxfp8_checkpoint": (_I32, [_P, _I64, _I64, _P, _P, _P, _P]),
@@ -643,8 +644,9 @@ def _width(t, name):
 def ep_entry_plan(tokens, top_k, device):
     """The plan under which grouped rows are the entries themselves, row t*top_k + j
     for slot j of token t: ``ep_bf16_combine`` takes ``ep_nvfp4_expert_matvec``'s
-    output [T, k, N], viewed [T*k, N], with it.  Depends on the sizes alone; unused
-    slots need no mark in it, their rows being zero."""
+    output [T, k, N], viewed [T*k, N], with it.  Depends on the sizes alone, so it names
+    every slot: where the routing leaves some unused, hand ``ep_bf16_combine`` the
+    routing's ids as well, or an unused slot's weight still meets its (zero) row."""
     i32 = dict(dtype=torch.int32, device=device)
     n = tokens * top_k
     return dict(counts=torch.full((1,), n, **i32), offsets=torch.tensor([0, n], **i32),
@@ -668,11 +670,13 @@ def ep_bf16_dispatch(x, plan, out=None):
     return out
 
 
-def ep_bf16_combine(rows, plan, weights=None, out=None):
+def ep_bf16_combine(rows, plan, weights=None, out=None, topk_idx=None, num_experts=None):
     """Grouped BF16 rows [r_cap, H] back to their tokens: out[t] = sum over slots j
     of weights[t, j] * rows[dst_row[t, j]] (FP32 sum, BF16 [T, H]); ``weights``
     float32 [T, k], or None for a plain sum (the gradient of ``ep_bf16_dispatch``).
-    Unused slots add nothing; padding rows are not read."""
+    Unused slots add nothing; padding rows are not read.  ``topk_idx`` [T, k] (int32
+    or int64) and ``num_experts``: slots whose id lies outside [0, num_experts) are
+    unused too, for a plan that does not mark them (``ep_entry_plan``)."""
     index, h = _index(rows), _width(rows, "rows")
     r_cap, t, k = _slots(plan, index)
     _want(rows, _BF16, "rows", index, (r_cap, h))
@@ -682,8 +686,15 @@ def ep_bf16_combine(rows, plan, weights=None, out=None):
         out = rows.new_empty((t, h))
     else:
         _want(out, _BF16, "out", index, (t, h))
-    _launch(index, "ep_bf16_combine", rows.data_ptr(), r_cap, h, t, k, plan["dst_row"].data_ptr(),
-            None if weights is None else weights.data_ptr(), out.data_ptr())
+    wp = None if weights is None else weights.data_ptr()
+    if topk_idx is None:
+        _launch(index, "ep_bf16_combine", rows.data_ptr(), r_cap, h, t, k, plan["dst_row"].data_ptr(), wp, out.data_ptr())
+        return out
+    idt = _topk(topk_idx)
+    if num_experts is None or topk_idx.get_device() != index or topk_idx.shape != (t, k):
+        raise ValueError(f"topk_idx must be [{t}, {k}] on rows' GPU, as the plan has them, and come with num_experts")
+    _launch(index, "ep_bf16_combine_topk", rows.data_ptr(), r_cap, h, t, k, plan["dst_row"].data_ptr(),
+            topk_idx.data_ptr(), idt, num_experts, wp, out.data_ptr())
     return out
 
 

@@ -90,15 +90,30 @@ __global__ __launch_bounds__(256) void k_bf16_dispatch(const uint16_t* __restric
   }
 }
 
+// The grouped row of a slot; none (-1) where the routing's id of the slot names no
+// expert (IDX void: no ids, the map alone says which slots are used).
+template <typename IDX>
+__device__ __forceinline__ int slot_row(const int32_t* __restrict__ dst_row, const IDX* __restrict__ ids, int E,
+                                        size_t slot) {
+  const int g = dst_row[slot];
+  if constexpr (std::is_void_v<IDX>) {
+    return g;
+  } else {
+    const IDX id = ids[slot];
+    return id >= 0 && id < E ? g : -1;
+  }
+}
+
 // out[t] = sum over slots j, in order, of w[t, j] * rows[dst_row[t, j]], in
 // FP32, rounded once.  One wave per token and 512 columns; the token is the
 // same in every lane, so its slots are scalars, and the loads of KU slots go
 // out before the first is used (one slot at a time, with a wave per block and
 // 2-byte loads, took 1072 us at 16384 x 7168, top-8).  Bound by memory: 2115 MB
 // in 357 us are 5.9 TB/s, where a large copy reaches 5.0.
-template <int KU, bool STREAM>
+template <int KU, bool STREAM, typename IDX>
 __global__ __launch_bounds__(256) void k_bf16_combine(const uint16_t* __restrict__ rows, int r_cap, int H, int k,
                                                       int segs, int waves, const int32_t* __restrict__ dst_row,
+                                                      const IDX* __restrict__ ids, int E,
                                                       const float* __restrict__ weights, uint16_t* __restrict__ out) {
   const int wv = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * 4u + (threadIdx.x >> 6)));
   int t, c;
@@ -110,7 +125,7 @@ __global__ __launch_bounds__(256) void k_bf16_combine(const uint16_t* __restrict
     bool used[KU];
 #pragma unroll
     for (int u = 0; u < KU; ++u) {
-      const int g = j0 + u < k ? dst_row[slot0 + j0 + u] : -1;
+      const int g = j0 + u < k ? slot_row(dst_row, ids, E, slot0 + j0 + u) : -1;
       used[u] = (uint32_t)g < (uint32_t)r_cap;
       if (used[u]) v[u] = ld8<STREAM>(rows + (size_t)g * H + c);
     }
@@ -214,11 +229,12 @@ __global__ __launch_bounds__(256) void k_bf16_combine_bwd(const uint16_t* __rest
 
 // Widths below one piece: a lane per token, value by value.
 enum Narrow { kNarrowDispatch, kNarrowCombine, kNarrowCombineBwd };
-template <Narrow OP>
+template <Narrow OP, typename IDX>
 __global__ __launch_bounds__(256) void k_bf16_narrow(const uint16_t* __restrict__ x, const uint16_t* __restrict__ rows,
                                                      int T, int H, int k, int r_cap, int pad_blocks,
                                                      const int32_t* __restrict__ dst_row,
                                                      const int32_t* __restrict__ src_row,
+                                                     const IDX* __restrict__ ids, int E,
                                                      const float* __restrict__ weights, uint16_t* __restrict__ out,
                                                      float* __restrict__ dweights) {
   if ((int)blockIdx.x < pad_blocks) {
@@ -231,7 +247,7 @@ __global__ __launch_bounds__(256) void k_bf16_narrow(const uint16_t* __restrict_
   float acc[kPiece] = {};
   for (int j = 0; j < k; ++j) {
     const size_t slot = (size_t)t * k + j;
-    const int g = dst_row[slot];
+    const int g = slot_row(dst_row, ids, E, slot);
     const bool used = (uint32_t)g < (uint32_t)r_cap;
     const size_t at = (size_t)(used ? g : 0) * H;
     const float w = OP != kNarrowDispatch && weights && used ? weights[slot] : 1.0f;
@@ -268,6 +284,33 @@ int32_t check_sizes(int64_t tokens, int64_t hidden, int64_t top_k, int64_t r_cap
 
 // Reads of more than the MALL holds are streamed.
 bool streamed(int64_t entries, int64_t hidden) { return entries * hidden * 2 > ((int64_t)256 << 20); }
+
+struct Combine {
+  const uint16_t* rows;
+  const int32_t* dst_row;
+  const float* weights;
+  uint16_t* out;
+  int R, H, T, k;
+  hipStream_t s;
+};
+
+template <bool STREAM, typename IDX>
+int32_t launch_combine(const Combine& c, const IDX* ids, int E) {
+  if (c.H < kPiece) {
+    hipLaunchKernelGGL((k_bf16_narrow<kNarrowCombine, IDX>), dim3((unsigned)((c.T + 255) / 256)), dim3(256), 0, c.s,
+                       nullptr, c.rows, c.T, c.H, c.k, c.R, 0, c.dst_row, nullptr, ids, E, c.weights, c.out, nullptr);
+    return launch_status();
+  }
+  const int segs = (c.H + kWaveCols - 1) / kWaveCols, waves = c.T * segs;
+  const dim3 grid((unsigned)((waves + 3) / 4)), block(256);
+  if (c.k <= 2)
+    hipLaunchKernelGGL((k_bf16_combine<2, STREAM, IDX>), grid, block, 0, c.s, c.rows, c.R, c.H, c.k, segs, waves,
+                       c.dst_row, ids, E, c.weights, c.out);
+  else
+    hipLaunchKernelGGL((k_bf16_combine<8, STREAM, IDX>), grid, block, 0, c.s, c.rows, c.R, c.H, c.k, segs, waves,
+                       c.dst_row, ids, E, c.weights, c.out);
+  return launch_status();
+}
 }  // namespace
 
 MTB_EXPORT int32_t ep_bf16_dispatch(const uint16_t* x, int64_t tokens, int64_t hidden, int64_t top_k, int64_t r_cap,
@@ -280,8 +323,9 @@ MTB_EXPORT int32_t ep_bf16_dispatch(const uint16_t* x, int64_t tokens, int64_t h
   const int T = (int)tokens, H = (int)hidden, R = (int)r_cap;
   const int pad_blocks = (R + kPadRows - 1) / kPadRows;
   if (H < kPiece) {
-    hipLaunchKernelGGL(k_bf16_narrow<kNarrowDispatch>, dim3((unsigned)(pad_blocks + (T + 255) / 256)), dim3(256), 0, s,
-                       x, nullptr, T, H, (int)top_k, R, pad_blocks, dst_row, src_row, nullptr, out, nullptr);
+    hipLaunchKernelGGL((k_bf16_narrow<kNarrowDispatch, void>), dim3((unsigned)(pad_blocks + (T + 255) / 256)),
+                       dim3(256), 0, s, x, nullptr, T, H, (int)top_k, R, pad_blocks, dst_row, src_row, nullptr, 0,
+                       nullptr, out, nullptr);
     return launch_status();
   }
   const int segs = (H + kWaveCols - 1) / kWaveCols, waves = T * segs;
@@ -297,26 +341,25 @@ MTB_EXPORT int32_t ep_bf16_combine(const uint16_t* rows, int64_t r_cap, int64_t 
   if (st != EP_OK) return st;
   if (tokens == 0) return EP_OK;
   if (!dst_row || !out || (r_cap > 0 && !rows)) return EP_ERR_NULL;
-  hipStream_t s = (hipStream_t)stream;
-  const int T = (int)tokens, H = (int)hidden, k = (int)top_k, R = (int)r_cap;
-  if (H < kPiece) {
-    hipLaunchKernelGGL(k_bf16_narrow<kNarrowCombine>, dim3((unsigned)((T + 255) / 256)), dim3(256), 0, s, nullptr,
-                       rows, T, H, k, R, 0, dst_row, nullptr, weights, out, nullptr);
-    return launch_status();
-  }
-  const int segs = (H + kWaveCols - 1) / kWaveCols, waves = T * segs;
-  const dim3 grid((unsigned)((waves + 3) / 4)), block(256);
-#define MTB_COMBINE(KU, ST) \
-  hipLaunchKernelGGL((k_bf16_combine<KU, ST>), grid, block, 0, s, rows, R, H, k, segs, waves, dst_row, weights, out)
-  if (streamed(tokens * top_k, hidden)) {
-    if (k <= 2) MTB_COMBINE(2, true);
-    else MTB_COMBINE(8, true);
-  } else {
-    if (k <= 2) MTB_COMBINE(2, false);
-    else MTB_COMBINE(8, false);
-  }
-#undef MTB_COMBINE
-  return launch_status();
+  const Combine c{rows, dst_row, weights, out, (int)r_cap, (int)hidden, (int)tokens, (int)top_k, (hipStream_t)stream};
+  return streamed(tokens * top_k, hidden) ? launch_combine<true, void>(c, nullptr, 0)
+                                          : launch_combine<false, void>(c, nullptr, 0);
+}
+
+MTB_EXPORT int32_t ep_bf16_combine_topk(const uint16_t* rows, int64_t r_cap, int64_t hidden, int64_t tokens,
+                                        int64_t top_k, const int32_t* dst_row, const void* topk_idx,
+                                        int32_t idx_dtype, int64_t num_experts, const float* weights, uint16_t* out,
+                                        void* stream) {
+  const int32_t st = check_sizes(tokens, hidden, top_k, r_cap);
+  if (st != EP_OK) return st;
+  if (num_experts < 1 || num_experts > 1024) return EP_ERR_SHAPE;
+  if (idx_dtype != EP_IDX_INT32 && idx_dtype != EP_IDX_INT64) return EP_ERR_DTYPE;
+  if (tokens == 0) return EP_OK;
+  if (!dst_row || !topk_idx || !out || (r_cap > 0 && !rows)) return EP_ERR_NULL;
+  const Combine c{rows, dst_row, weights, out, (int)r_cap, (int)hidden, (int)tokens, (int)top_k, (hipStream_t)stream};
+  // not streamed: its rows are a few tokens' expert products, which the caches still hold
+  return idx_dtype == EP_IDX_INT64 ? launch_combine<false>(c, (const int64_t*)topk_idx, (int)num_experts)
+                                   : launch_combine<false>(c, (const int32_t*)topk_idx, (int)num_experts);
 }
 
 MTB_EXPORT int32_t ep_bf16_combine_bwd(const uint16_t* dout, const uint16_t* rows, int64_t tokens, int64_t hidden,
@@ -331,8 +374,9 @@ MTB_EXPORT int32_t ep_bf16_combine_bwd(const uint16_t* dout, const uint16_t* row
   const int T = (int)tokens, H = (int)hidden, k = (int)top_k, R = (int)r_cap;
   const int pad_blocks = (R + kPadRows - 1) / kPadRows;
   if (H < kPiece) {
-    hipLaunchKernelGGL(k_bf16_narrow<kNarrowCombineBwd>, dim3((unsigned)(pad_blocks + (T + 255) / 256)), dim3(256), 0,
-                       s, dout, rows, T, H, k, R, pad_blocks, dst_row, src_row, weights, drows, dweights);
+    hipLaunchKernelGGL((k_bf16_narrow<kNarrowCombineBwd, void>), dim3((unsigned)(pad_blocks + (T + 255) / 256)),
+                       dim3(256), 0, s, dout, rows, T, H, k, R, pad_blocks, dst_row, src_row, nullptr, 0, weights,
+                       drows, dweights);
     return launch_status();
   }
 #define MTB_BWD(NP, KU, ST)                                                                                          \

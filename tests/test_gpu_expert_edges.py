@@ -1,4 +1,5 @@
-"""The expert layer's calls at their edges on the GPU: empty batches."""
+"""The expert layer's calls at their edges on the GPU: empty batches, weights of
+unused slots that are not numbers.  Bounds are those of ``test_gpu_expert``."""
 
 import os
 import sys
@@ -8,9 +9,10 @@ import pytest
 import torch
 
 import moe_token_block_amd as mtb
+from oracle import expert
 
-from gpu_util import require_gpu, host
-from test_gpu_expert import _weights
+from gpu_util import require_gpu, bf16_dev, host, assert_bytes_equal
+from test_gpu_expert import U, _bits, _ids, _near, _plan, _weights
 
 sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
 import expert_layer as ex  # noqa: E402
@@ -51,3 +53,77 @@ def test_serving_no_tokens(dev):
     dx, act2 = mtb.dswiglu_mxfp8_checkpoint(data, scales, act)
     assert dx.shape == (0, 128) and act2.shape == act.shape == (0, 64)
     assert mtb.ep_mxfp8_unpack(data, scales).shape == (0, 128)
+
+
+# ------------------------------------------------------------------ unused slots
+@pytest.mark.parametrize("idt", [np.int32, np.int64])
+@pytest.mark.parametrize("t,e,k,h", [(1, 4, 2, 4096), (6, 4, 2, 5), (9, 12, 9, 7), (40, 3, 1, 8), (33, 6, 2, 521),
+                                     (21, 16, 8, 1024), (70, 5, 3, 1001)])
+def test_combine_of_entries_with_unused_slots(dev, idt, t, e, k, h):
+    # the entries' plan names every slot: those whose id names no expert add nothing, whatever their weight and row hold
+    rng = np.random.default_rng(t * h + k)
+    ids = _ids(rng, t, e, k, 0.4).astype(idt)
+    ids[0, 0] = e                                             # no expert, nor is -2 or (64 bits) 2^32
+    ids[-1, -1] = -2 if idt is np.int32 else 2 ** 32
+    used = (ids >= 0) & (ids < e)
+    rows, w = _bits(rng.standard_normal((t * k, h))), rng.standard_normal((t, k)).astype(np.float32)
+    rows[~used.reshape(-1)] = 0x7FC0
+    w[~used] = rng.choice([np.nan, np.inf, -np.inf], size=(~used).sum())
+    dst = np.where(used, np.arange(t * k).reshape(t, k), -1).astype(np.int32)
+    rd, wd, idd = bf16_dev(rows, dev), torch.from_numpy(w).to(dev), torch.from_numpy(ids).to(dev)
+    entries = mtb.ep_entry_plan(t, k, dev)
+    got = mtb.ep_bf16_combine(rd, entries, wd, topk_idx=idd, num_experts=e)
+    want, mag = expert.combine(expert.f64(rows), dst, w)
+    _near(got, want, (k + 1) * U * mag, "weighted")
+    marked = dict(entries, dst_row=torch.from_numpy(dst).to(dev))
+    assert_bytes_equal(host(got), host(mtb.ep_bf16_combine(rd, marked, wd)), "a plan that marks them")
+    want, mag = expert.combine(expert.f64(rows), dst)
+    _near(mtb.ep_bf16_combine(rd, entries, topk_idx=idd, num_experts=e), want, (k + 1) * U * mag, "without weights")
+
+
+def test_combine_takes_both_the_plans_marks_and_the_ids(dev):
+    rng = np.random.default_rng(2)
+    t, e, k, h = 19, 5, 2, 72
+    ids = _ids(rng, t, e, k, 0.3)
+    plan = _plan(ids, e, 16, dev)
+    fewer = np.where(rng.random(ids.shape) < 0.3, -1, np.abs(ids)).astype(np.int32)  # |-1| = 1 names an expert again
+    dst = np.where(fewer >= 0, host(plan["dst_row"]), -1)
+    rows, w = _bits(rng.standard_normal((plan["r_cap"], h))), rng.standard_normal((t, k)).astype(np.float32)
+    w[dst < 0] = np.nan
+    got = mtb.ep_bf16_combine(bf16_dev(rows, dev), plan, torch.from_numpy(w).to(dev),
+                              topk_idx=torch.from_numpy(fewer).to(dev), num_experts=e)
+    want, mag = expert.combine(expert.f64(rows), dst, w)
+    _near(got, want, (k + 1) * U * mag, "combine")
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_serving_with_a_weight_that_is_no_number_in_an_unused_slot(dev, bad):
+    torch.manual_seed(3)
+    t, h, f, e, k = 5, 256, 128, 4, 2
+    layer = ex.ExpertLayer(e, h, f, dev, seed=1)
+    x = torch.randn(t, h, device=dev).bfloat16()
+    top = torch.topk(torch.randn(t, e, device=dev), k)
+    ids, w = top.indices.int(), torch.softmax(top.values, 1)
+    ids[1] = -1                                               # a token with no expert at all
+    ids[3, 1] = -1
+    clean = w.masked_fill(ids < 0, 0.0)
+    packed, entries = layer.pack(), mtb.ep_entry_plan(t, k, dev)
+    got = ex.serve(x, ids, w.masked_fill(ids < 0, bad), packed, entries)
+    assert_bytes_equal(host(got), host(ex.serve(x, ids, clean, packed, entries)), "served")
+    assert not host(got)[1].any() and bool(torch.isfinite(got.float()).all())
+    # as the training path has it
+    out, _ = layer.forward(x, ids, w.masked_fill(ids < 0, bad))
+    assert not host(out)[1].any() and bool(torch.isfinite(out.float()).all())
+
+
+def test_combine_refuses_ids_that_do_not_fit(dev):
+    rows = torch.zeros((6, 16), dtype=torch.bfloat16, device=dev)
+    entries = mtb.ep_entry_plan(3, 2, dev)
+    ids = torch.zeros((3, 2), dtype=torch.int32, device=dev)
+    for kw in (dict(topk_idx=ids), dict(topk_idx=ids[:2], num_experts=4), dict(topk_idx=ids.cpu(), num_experts=4),
+               dict(topk_idx=ids.float(), num_experts=4), dict(topk_idx=ids.view(6), num_experts=4),
+               dict(topk_idx=ids.t().contiguous().t(), num_experts=4), dict(topk_idx=ids, num_experts=0),
+               dict(topk_idx=ids, num_experts=1025)):
+        with pytest.raises((ValueError, TypeError, mtb.EpError)):
+            mtb.ep_bf16_combine(rows, entries, **kw)
+            raise AssertionError(f"{kw} was not refused")
