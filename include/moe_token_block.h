@@ -560,7 +560,9 @@ int32_t ep_nvfp4_expert_matvec(const uint16_t* x, int64_t tokens, int64_t hidden
 /* SwiGLU whose pre-activation is kept in MXFP8 for the backward pass (33 bytes
  * per 32 values instead of 64):
  *   act = silu(a) * b of the BF16 preact = [a | b], computed in FP32 and rounded
- *   to BF16; data and scales: the bytes ep_mxfp8_pack gives for preact.
+ *   to BF16; data and scales: the bytes ep_mxfp8_pack gives for preact, but
+ *   for blocks of 32 with an infinity or a NaN: their scale byte is 255, so that
+ *   the whole block reads back as NaN.
  *   preact [tokens, 2*ffn], act [tokens, ffn], data [tokens, 2*ffn], scales
  *   [tokens, 2*ffn/32].  Requires ffn a positive multiple of 32, at most 2^24,
  *   and tokens * ffn < 2^34 (EP_ERR_RANGE). */

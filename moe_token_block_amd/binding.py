@@ -769,8 +769,8 @@ def ep_nvfp4_expert_matvec(x, weight, topk_idx=None, swiglu=False, out=None, d_e
 # ------------------------------------------------------------------ SwiGLU with an 8-bit checkpoint
 def swiglu_mxfp8_checkpoint(preact, act=None, data=None, scales=None):
     """act = silu(a) * b of BF16 preact [T, 2F] = [a | b], and preact kept as MXFP8
-    (the bytes of ``ep_mxfp8_pack``): (act BF16 [T, F], data uint8 [T, 2F], scales
-    uint8 [T, 2F/32])."""
+    (the bytes of ``ep_mxfp8_pack``; a block of 32 that is not finite reads back as
+    NaN): (act BF16 [T, F], data uint8 [T, 2F], scales uint8 [T, 2F/32])."""
     index = _index(preact)
     if preact.dim() != 2 or preact.shape[1] % 64:
         raise ValueError("preact must be [tokens, 2*ffn] with ffn a multiple of 32")

@@ -57,9 +57,12 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
 }
 
 // Eight values of a 32-value block, whose largest magnitude is m, as E4M3 bytes;
-// the block's exponent.
-__device__ __forceinline__ u32x2 quantize8(u32x4 v, uint32_t m, int& e) {
-  e = mx_exponent(__uint_as_float(m << 16));
+// the block's scale byte.  A block with an infinity or a NaN gets E8M0's NaN: its
+// exponent would be made up and the infinity kept as a finite value, so that the
+// gradient hid what the output shows.
+__device__ __forceinline__ u32x2 quantize8(u32x4 v, uint32_t m, uint8_t& scale) {
+  const int e = mx_exponent(__uint_as_float(m << 16));
+  scale = (uint8_t)(m < 0x7F80u ? e + 127 : 255);
   if (e >= -126) {
     const float s = pow2f(e);
     return u32x2{fp8x4_from_bf16(v[0], v[1], s), fp8x4_from_bf16(v[2], v[3], s)};
@@ -78,14 +81,14 @@ __global__ __launch_bounds__(256) void k_swiglu_checkpoint(const uint16_t* __res
   if (i >= chunks) return;  // whole quads: chunks is a multiple of 4
   const size_t ca = (size_t)i + (size_t)(i / nch) * nch, cb = ca + nch;  // chunks of a and b within [T, 2F/8]
   const u32x4 a = ld_once<u32x4>(preact + 8 * ca), b = ld_once<u32x4>(preact + 8 * cb);
-  int ea, eb;
+  uint8_t ea, eb;
   const u32x2 da = quantize8(a, quad_max(absmax_bf16x8(make_uint4(a[0], a[1], a[2], a[3]))), ea);
   const u32x2 db = quantize8(b, quad_max(absmax_bf16x8(make_uint4(b[0], b[1], b[2], b[3]))), eb);
   st_once(data + 8 * ca, da);
   st_once(data + 8 * cb, db);
   if ((i & 3) == 0) {
-    scales[ca >> 2] = (uint8_t)(ea + 127);
-    scales[cb >> 2] = (uint8_t)(eb + 127);
+    scales[ca >> 2] = ea;
+    scales[cb >> 2] = eb;
   }
   u32x4 y;
 #pragma unroll

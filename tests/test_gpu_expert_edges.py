@@ -1,5 +1,5 @@
 """The expert layer's calls at their edges on the GPU: empty batches, weights of
-unused slots that are not numbers.  Bounds are those of ``test_gpu_expert``."""
+unused slots that are not numbers, pre-activations that are not finite.  Bounds are those of ``test_gpu_expert``."""
 
 import os
 import sys
@@ -9,10 +9,10 @@ import pytest
 import torch
 
 import moe_token_block_amd as mtb
-from oracle import expert
+from oracle import expert, mxfp8
 
 from gpu_util import require_gpu, bf16_dev, host, assert_bytes_equal
-from test_gpu_expert import U, _bits, _ids, _near, _plan, _weights
+from test_gpu_expert import U, _act_slack, _bits, _grad_slack, _ids, _near, _plan, _weights
 
 sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
 import expert_layer as ex  # noqa: E402
@@ -127,3 +127,50 @@ def test_combine_refuses_ids_that_do_not_fit(dev):
         with pytest.raises((ValueError, TypeError, mtb.EpError)):
             mtb.ep_bf16_combine(rows, entries, **kw)
             raise AssertionError(f"{kw} was not refused")
+
+
+# ------------------------------------------------------------------ pre-activations that are not finite
+@pytest.mark.parametrize("t,f", [(1, 32), (4, 96), (9, 1024)])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan"), -float("nan")])
+def test_checkpoint_of_a_block_that_is_not_finite(dev, t, f, bad):
+    # such a block of 32 comes back as NaN, whole, so that the gradient shows what the output does; the others keep
+    # their bytes
+    rng = np.random.default_rng(t + f)
+    p = rng.standard_normal((t, 2 * f)).astype(np.float32) * 3
+    p[0, 0:32] = 0.0                                          # a block of zeros but for the one value
+    clean = _bits(p)
+    p[0, 5] = bad                                             # in a gate
+    p[-1, f + 31] = bad                                       # and in an up value
+    where = np.zeros((t, 2 * f), dtype=bool)
+    where[0, 0:32] = where[-1, f : f + 32] = True
+    pb, dyb = _bits(p), _bits(rng.standard_normal((t, f)))
+    pb[0, 5] = np.uint16(torch.tensor(bad).bfloat16().view(torch.int16).item() & 0xFFFF)
+    pb[-1, f + 31] = pb[0, 5]
+    act, data, scales = mtb.swiglu_mxfp8_checkpoint(bf16_dev(pb, dev))
+    wd, ws = mxfp8.pack_rows(clean)
+    blocks = where[:, ::32]
+    assert np.all(host(scales)[blocks] == 255)
+    assert_bytes_equal(host(scales)[~blocks], ws[~blocks], "scales of the other blocks")
+    assert_bytes_equal(host(data)[~where], wd[~where], "data of the other blocks")
+    back = host(mtb.ep_mxfp8_unpack(data, scales))
+    assert np.all((back[where] & 0x7FFF) > 0x7F80) and np.all((back[~where] & 0x7F80) < 0x7F80)
+    # the output follows the formula value by value
+    a = expert.f64(clean)
+    want, slack = expert.swiglu(a), _act_slack(a)
+    hit = np.zeros((t, f), dtype=bool)
+    hit[0, 5] = hit[-1, 31] = True
+    got = host(act).copy()
+    assert np.all((got[hit] & 0x7FFF) >= 0x7F80)
+    got[hit] = host(mtb.swiglu_mxfp8_checkpoint(bf16_dev(clean, dev))[0])[hit]
+    _near(got, want, slack, "act")
+    # the gradient: NaN wherever the block is an argument (db = dy * silu(a) has none of b's), the formula elsewhere
+    dx, act2 = mtb.dswiglu_mxfp8_checkpoint(data, scales, bf16_dev(dyb, dev))
+    lost = where[:, :f] | where[:, f:]
+    dxn, actn = np.isnan(expert.f64(host(dx))), np.isnan(expert.f64(host(act2)))
+    np.testing.assert_array_equal(actn, lost)
+    np.testing.assert_array_equal(dxn, np.concatenate([lost, where[:, :f]], 1))
+    v, dy = mxfp8.decode(wd, ws), expert.f64(dyb)
+    got = host(dx).copy()
+    want, slack = expert.swiglu_grad(v, dy), _grad_slack(v, dy)
+    got[dxn] = _bits(want)[dxn]
+    _near(got, want, slack, "dx")
