@@ -75,6 +75,18 @@ __device__ __forceinline__ float block_scale(uint32_t s, int b) {
                   : __builtin_amdgcn_cvt_f32_fp8((int)s, 3);
 }
 
+// What a weight row is decoded with in place of its t, and what its sums are
+// multiplied by.  Below t = 2^-32 every row is taken at 2^-32 instead: its weights
+// are normal BF16 numbers then (the least is 2^-10 t, which small rows would lose),
+// and no sum of up to 2^20 products with the largest activations leaves FP32's
+// range (2^20 * 2688 * 2^-32 * 2^128 < 2^128).  Both steps are exact.
+__device__ __forceinline__ float lift_row(float& t) {
+  const bool small = t < 0x1p-32f;
+  const float post = small ? t * 0x1p32f : 1.0f;
+  t = small ? 0x1p-32f : t;
+  return post;
+}
+
 // A tile's rows as a buffer: 16 from row `row` of expert e on, or fewer where the
 // rows end; what lies past them reads as zeros.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rows(const uint8_t* weight, size_t first, int rows, uint32_t rb) {
@@ -228,14 +240,9 @@ __global__ __launch_bounds__(512) void k_nvfp4_matvec(const uint16_t* __restrict
     for (int i = tid; i < M; i += blockDim.x) list[i] = xrows[i] = (uint16_t)i;
     __syncthreads();
   }
-  // a row of tiny weights is taken 2^64 times larger, so that each is a normal
-  // BF16 number, and its sums scaled back (post)
   float post[RT];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    post[i] = t[i] < 0x1p-64f ? 0x1p-64f : 1.0f;
-    t[i] = t[i] < 0x1p-64f ? t[i] * 0x1p64f : t[i];
-  }
+  for (int i = 0; i < RT; ++i) post[i] = lift_row(t[i]);
 
   const int first = 16 * (int)blockIdx.z;
   for (int c0 = first; c0 < n; c0 += 16 * (int)gridDim.z) {
@@ -386,9 +393,7 @@ __global__ __launch_bounds__(256, 2) void k_nvfp4_matvec_wide(const uint16_t* __
     const int row0 = min(col0 + 16 * (wave * GT + i % GT), NO);
     rows[i] = tile_rows(weight, (size_t)e * N + row0 + (SWIGLU && i >= GT ? NO : 0), NO - row0, rb);
     t[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rows[i], (int)((uint32_t)r * rb + (K >> 1) + (K >> 4)), 0, 0));
-    // rows of tiny weights: as above
-    posts[wave][i][r] = t[i] < 0x1p-64f ? 0x1p-64f : 1.0f;
-    t[i] = t[i] < 0x1p-64f ? t[i] * 0x1p64f : t[i];
+    posts[wave][i][r] = lift_row(t[i]);
   }
   const uint32_t code = (uint32_t)(r & ~3) * rb + 16u * (4 * g + (r & 3)), scale = (uint32_t)r * rb + (K >> 1) + 8 * g;
   auto load_w = [&](int kb, WTile* w) {

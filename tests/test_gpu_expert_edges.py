@@ -1,5 +1,6 @@
 """The expert layer's calls at their edges on the GPU: empty batches, weights of
-unused slots that are not numbers, pre-activations that are not finite.  Bounds are those of ``test_gpu_expert``."""
+unused slots that are not numbers, pre-activations that are not finite, small
+weights times large activations.  Bounds are those of ``test_gpu_expert``."""
 
 import os
 import sys
@@ -9,10 +10,10 @@ import pytest
 import torch
 
 import moe_token_block_amd as mtb
-from oracle import expert, mxfp8
+from oracle import expert, mxfp8, nvfp4
 
 from gpu_util import require_gpu, bf16_dev, host, assert_bytes_equal
-from test_gpu_expert import U, _act_slack, _bits, _grad_slack, _ids, _near, _plan, _weights
+from test_gpu_expert import U, _act_slack, _bits, _check_matvec, _grad_slack, _ids, _near, _plan, _weights
 
 sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
 import expert_layer as ex  # noqa: E402
@@ -174,3 +175,21 @@ def test_checkpoint_of_a_block_that_is_not_finite(dev, t, f, bad):
     want, slack = expert.swiglu_grad(v, dy), _grad_slack(v, dy)
     got[dxn] = _bits(want)[dxn]
     _near(got, want, slack, "dx")
+
+
+# ------------------------------------------------------------------ small weights, large activations
+# tokens, experts, width, hidden: a block's few rows, blocks of more waves, and the kernel for many entries
+@pytest.mark.parametrize("t,e,n,k", [(3, 1, 24, 192), (70, 20, 514, 128), (288, 16, 2050, 64)])
+@pytest.mark.parametrize("scale,x_scale", [(2.0 ** -62, 2.0 ** 126), (2.0 ** -55, 2.0 ** 126), (2.0 ** -22, 2.0 ** 126),
+                                           (2.0 ** -24, 2.0 ** -80), (2.0 ** -110, 2.0 ** 20)])
+def test_matvec_of_small_weights_and_large_activations(dev, t, e, n, k, scale, x_scale):
+    # sums that are ordinary numbers, or large ones, may not leave FP32's range on the way
+    rng = np.random.default_rng(t)
+    w = nvfp4.pack_rows(_bits(rng.standard_normal((e * n, k)) * scale)).reshape(e, n, -1)
+    xb = _bits(np.clip(rng.standard_normal((t, k)), -1.9, 1.9) * x_scale)
+    ids = (rng.permutation(t) % e).astype(np.int32)[:, None]
+    print(f"small weights {t} {e} {n} {k} {scale} {x_scale}", flush=True)
+    got = mtb.ep_nvfp4_expert_matvec(bf16_dev(xb, dev), torch.from_numpy(w).to(dev), torch.from_numpy(ids).to(dev))
+    y, _ = expert.matvec(expert.f64(xb), w, ids)
+    assert np.abs(y).max() < 2.0 ** 127
+    _check_matvec(got, expert.f64(xb), w, ids, False, f"scale {scale}")
