@@ -1,7 +1,8 @@
 """rocprofv3 summaries of the bench workloads, written under profiles/.
 
 Run on a machine with an MI355X and rocprofv3, from the repository root; this
-process itself never touches the GPU (every GPU run is a rocprofv3 child).
+process itself never touches the GPU (every GPU run is a rocprofv3 child), but as
+``expert-pass``, which is such a child.
 
   python rocprof_summaries.py counters [--configs 1,2,3,4,5] [--raw DIR]
       Per configuration, three rocprofv3 --pmc runs of `bench.py --counters-pass
@@ -22,6 +23,14 @@ process itself never touches the GPU (every GPU run is a rocprofv3 child).
       Kernel-trace statistics of `bench.py --workload cfgN` (all: of the default
       `bench.py`, the command that prints the headline line), with the timed
       step's dispatches -> profiles/kernel_trace_<workload>.md
+  python rocprof_summaries.py expert [--raw DIR]
+      The expert layer's calls at the cases of perf/operators.py and the further
+      ones below: per case, one rocprofv3 --kernel-trace run of `rocprof_summaries.py
+      expert-pass --case NAME` (a child that does use the GPU: passes over three
+      input sets in turn, untimed ones until the clock has settled, then 60 between
+      marker kernels), and one run of the child without the profiler, which times the
+      passes eager and in a graph -> profiles/kernel_times_expert_layer.md; for the NVFP4 products
+      also three --pmc runs of it -> profiles/counters_expert_matvec.md.
 """
 
 import argparse
@@ -340,21 +349,196 @@ def trace(args):
     print("wrote", path)
 
 
+# ------------------------------------------------------------------ the expert layer
+EXPERT_SOURCES = ("combine.hip", "common.h", "matvec.hip", "mxfp8.h", "swiglu.hip")
+EXPERT_GROUPS = (("FETCH_SIZE",), ("TCC_REQ_sum", "TCC_MISS_sum", "TCC_EA0_RDREQ_DRAM_sum"),
+                 ("SQ_INSTS_VALU", "SQ_ACTIVE_INST_VALU", "SQ_VALU_MFMA_BUSY_CYCLES", "SQ_BUSY_CU_CYCLES",
+                  "SQ_INSTS_LDS", "SQ_LDS_BANK_CONFLICT", "SQ_WAIT_INST_ANY", "SQ_WAVE_CYCLES"))
+EXPERT_PASSES = 60
+
+
+def expert_cases():
+    """The cases of perf/operators.py and, of the same operators, the forms that it
+    draws but does not list: routing skewed to a few experts, few weight rows with
+    many entries, and loads on both sides of the rule between the two kernels."""
+    from perf import operators as ops
+    mv = dict(op="matvec", dense=False, swiglu=False, per_entry=False, unused=0.0)
+    more = [dict(mv, name=f"matvec_{t}x7168_dense_7168", tokens=t, experts=1, top_k=1, n=7168, k=7168, dense=True)
+            for t in (8, 64, 128)]
+    more += [dict(mv, name=f"matvec_{t}x7168_e32_top8_swiglu{'_skewed' * s}", tokens=t, experts=32, top_k=8, n=4096,
+                  k=7168, swiglu=True, **(dict(skew=1.2) if s else {}))
+             for t, s in ((32, 0), (32, 1), (48, 0), (52, 0), (56, 0), (60, 0), (62, 0), (62, 1), (64, 0), (64, 1))]
+    return ops, ops.listed() + more
+
+
+def expert_state(ops, case, seed):
+    state = ops.prepare(case, seed)
+    if case.get("skew") and case["op"] == "matvec":  # the ids of the same skew that the row cases have
+        import torch
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        state["ids"] = ops._routing(g, case["tokens"], case["experts"], case["top_k"], case["skew"], 0.0)[0]
+    return state
+
+
+def expert_pass(args):
+    """The profiled child: one case's passes between two marker kernels (digamma, used nowhere else)."""
+    import torch
+    ops, cases = expert_cases()
+    ops.own = True
+    case = next(c for c in cases if c["name"] == args.case)
+    states = [expert_state(ops, case, seed) for seed in range(3)]
+    mark = torch.ones(1, device="cuda")
+    t0, n = time.monotonic(), 0
+    while n < 3 or (time.monotonic() - t0 < args.settle_s and n < 20000):
+        ops.run(states[n % 3])
+        n += 1
+        if n % 50 == 0:
+            torch.cuda.synchronize()
+    mark.digamma()
+    for i in range(EXPERT_PASSES):
+        ops.run(states[i % 3])
+    mark.digamma()
+    torch.cuda.synchronize()
+    us, graph_us = None, None
+    if args.timed:
+        def timed(passes, f):
+            best = []
+            for _ in range(7):
+                t0 = time.perf_counter()
+                f()
+                torch.cuda.synchronize()
+                best.append((time.perf_counter() - t0) / passes * 1e6)
+            return sorted(best)[3]
+
+        def eager():
+            for i in range(EXPERT_PASSES):
+                ops.run(states[i % 3])
+
+        us = timed(EXPERT_PASSES, eager)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for i in range(EXPERT_PASSES):
+                ops.run(states[i % 3])
+        timed(EXPERT_PASSES, graph.replay)
+        graph_us = timed(EXPERT_PASSES, graph.replay)
+    loads = None
+    if case["op"] == "matvec" and not case["dense"]:
+        c = torch.bincount(states[0]["ids"].reshape(-1).clamp(min=0).long(), minlength=case["experts"])
+        loads = [int(c.max()), float(c.float().mean())]
+    print(json.dumps({"case": args.case, "us": us, "graph_us": graph_us, "loads": loads, **ops.work(case)}), flush=True)
+
+
+def _expert_run(tool, case, out, settle):
+    """One profiled run of the child; its line, the trace's directory and the command as shown."""
+    child = ["rocprof_summaries.py", "expert-pass", "--settle-s", str(settle)]
+    tool = ["rocprofv3"] + tool + ["--output-format", "csv", "-d", "OUT", "-o", "run", "--"] if tool else []
+    child += [] if tool else ["--timed"]
+    text = run([out if a == "OUT" else a for a in tool] + [sys.executable, os.path.join(ROOT, child[0])] + child[1:]
+               + ["--case", case], 150)
+    shown = " ".join(tool + ["python3"] + child + ["--case", "NAME"])
+    return json.loads(next(ln for ln in text.splitlines() if ln.startswith('{"case"'))), shown
+
+
+def _between_marks(rows, name, order):
+    rows = sorted(rows, key=order)
+    marks = [i for i, r in enumerate(rows) if "digamma" in r[name]]
+    return rows[marks[0] + 1:marks[-1]]
+
+
+def expert(args):
+    import hashlib
+    raw = args.raw or tempfile.mkdtemp(prefix="mtb_expert_")
+    _, cases = expert_cases()
+    h = hashlib.sha256()
+    for f in EXPERT_SOURCES:
+        h.update(bench._code_only(open(os.path.join(ROOT, "moe_token_block_amd", "csrc", f)).read()).encode())
+    head = [f"Date {datetime.date.today().isoformat()}, `python rocprof_summaries.py expert`; sources "
+            f"({', '.join(EXPERT_SOURCES)}, code only) {h.hexdigest()[:16]}.  Commands (from the repository root, NAME "
+            "each case):", "", "```"]
+    shown, md = [], []
+    for c in cases:
+        out = os.path.join(raw, "trace_" + c["name"])
+        plain, untraced = _expert_run([], c["name"], out, 0.3)
+        line, traced = _expert_run(["--kernel-trace"], c["name"], out, 0.3)
+        shown = [untraced, traced]
+        rows = _between_marks(list(csv.DictReader(open(os.path.join(out, "run_kernel_trace.csv")))), "Kernel_Name",
+                              lambda r: int(r["Start_Timestamp"]))
+        per = {}
+        for r in rows:
+            per.setdefault((kernel_name(r["Kernel_Name"]), r["Grid_Size_X"], r["Grid_Size_Y"], r["Grid_Size_Z"],
+                            r["Workgroup_Size_X"]), []).append((int(r["End_Timestamp"]) - int(r["Start_Timestamp"])) / 1e3)
+        for i, ((nm, gx, gy, gz, wg), v) in enumerate(per.items()):
+            grid = " x ".join(str(g) for g in (int(gx) // int(wg), int(gy), int(gz)) if g > 1) or "1"
+            load = f" ({line['loads'][0]} entries on the fullest expert, mean {line['loads'][1]:.1f})" \
+                if line["loads"] and c["tokens"] > 8 and i == 0 else ""
+            md.append(f"| {c['name'] + load if i == 0 else ''} | `{nm}` | {grid} of {wg} | {np.median(v):.2f} | "
+                      f"{np.percentile(v, 25):.2f}-{np.percentile(v, 75):.2f} | {min(v):.2f} | "
+                      + (f"{plain['us']:.2f} | {plain['graph_us']:.2f} | {line['bytes'] / 1e6:.1f} | "
+                         f"{line['bytes'] / plain['graph_us'] / 1e6:.2f} |" if i == 0 else "| | | |"))
+    doc = ["# Times of the expert layer's calls", ""] + head + shown + ["```", "",
+           f"{EXPERT_PASSES} passes of each case over three input sets in turn, after 0.3 s of untimed passes.  Traced: "
+           "duration of each of the call's kernels, start to end.  Untraced, per pass, the median of seven runs: the "
+           "Python calls, and the same passes captured in one graph and replayed (no host time; a kernel's start "
+           "overlaps its predecessor's end, so that short ones take less than their traced duration).  Bytes: each "
+           "input and output once; TB/s: those over the time in a graph.", "",
+           "| case | kernel | blocks of threads | traced median us | IQR us | min us | calls us | in a graph us | MB | TB/s |",
+           "|---|---|---|---|---|---|---|---|---|---|"]
+    with open(os.path.join(args.out_dir, "kernel_times_expert_layer.md"), "w") as fh:
+        fh.write("\n".join(doc + md) + "\n")
+
+    ref = json.load(open(os.path.join(ROOT, "profiles", "counters.json")))["copy_reference"]
+    shown, md = [], []
+    for c in [c for c in cases if c["op"] == "matvec" and c["n"] * c["k"] > 1 << 22]:
+        got = {}
+        for g in EXPERT_GROUPS:
+            out = os.path.join(raw, f"pmc_{c['name']}_{g[0]}")
+            line, cmd = _expert_run(["--pmc"] + list(g), c["name"], out, 0.0)
+            if cmd not in shown:
+                shown.append(cmd)
+            rows = _between_marks(list(csv.DictReader(open(os.path.join(out, "run_counter_collection.csv")))),
+                                  "Kernel_Name", lambda r: int(r["Dispatch_Id"]))
+            for r in rows:
+                got[r["Counter_Name"]] = got.get(r["Counter_Name"], 0.0) + float(r["Counter_Value"]) / EXPERT_PASSES
+        md.append(f"| {c['name']} | {line['bytes'] / 1e6:.1f} | {got['TCC_MISS_sum'] * 128 / 1e6:.1f} | "
+                  f"{got['FETCH_SIZE'] * 1024 * ref['FETCH_SIZE'] / 1e6:.1f} | "
+                  f"{got['TCC_EA0_RDREQ_DRAM_sum'] * ref['TCC_EA0_RDREQ_DRAM_sum'] / 1e6:.1f} | "
+                  f"{got['TCC_REQ_sum'] * 128 / 1e6:.0f} | "
+                  f"{got['SQ_INSTS_VALU']:.4g} | {got['SQ_ACTIVE_INST_VALU']:.4g} | {got['SQ_VALU_MFMA_BUSY_CYCLES']:.4g} | "
+                  f"{got['SQ_BUSY_CU_CYCLES']:.4g} | {got['SQ_INSTS_LDS']:.4g} | {got['SQ_LDS_BANK_CONFLICT']:.4g} | "
+                  f"{got['SQ_WAIT_INST_ANY'] / got['SQ_WAVE_CYCLES']:.2f} | {line['flops'] / 1e9:.1f} |")
+    doc = ["# Counters of the NVFP4 expert products", ""] + head + shown + ["```", "",
+           f"Per pass, {EXPERT_PASSES} passes over three input sets in turn; summed over the counter's dimensions.  L2 misses "
+           "and requests in MB of 128-byte lines; bytes fetched past the L2 (FETCH_SIZE) and from DRAM, scaled by a 1 GiB "
+           "copy's as in counters.json; VALU wave-instructions, "
+           "active VALU cycles and busy MFMA cycles of all SIMDs, busy cycles of all CUs, LDS instructions and conflict "
+           "cycles; the share of a wave's cycles in which it waits for an instruction to issue or return; GFLOP.", "",
+           "| case | MB, each byte once | L2 miss MB | fetched MB | DRAM read MB | L2 request MB | VALU | VALU cycles | MFMA cycles | "
+           "CU cycles | LDS | LDS conflicts | waiting | GFLOP |",
+           "|---|---|---|---|---|---|---|---|---|---|---|---|---|---|"]
+    with open(os.path.join(args.out_dir, "counters_expert_matvec.md"), "w") as fh:
+        fh.write("\n".join(doc + md) + "\n")
+
+
 def main():
     p = argparse.ArgumentParser()
-    p.add_argument("what", choices=["counters", "kernels", "trace"])
+    p.add_argument("what", choices=["counters", "kernels", "trace", "expert", "expert-pass"])
+    p.add_argument("--case", default=None, help="expert-pass: the case's name")
+    p.add_argument("--timed", action="store_true", help="expert-pass: time the passes too, eager and in a graph")
+    p.add_argument("--settle-s", type=float, default=0.0, help="expert-pass: seconds of passes before the recorded ones")
     p.add_argument("--workload", default="cfg3", choices=list(WORKLOAD_NAMES) + ["all"])
     p.add_argument("--configs", default="1,2,3,4,5")
     p.add_argument("--raw", default=None, help="directory for rocprofv3's raw output (default: a temp dir)")
     p.add_argument("--steps", type=int, default=20)
     p.add_argument("--out-dir", default=os.path.join(ROOT, "profiles"), help="where the summaries go")
     args = p.parse_args()
+    if args.what == "expert-pass":
+        return expert_pass(args)
     args.out_dir = os.path.abspath(args.out_dir)
     os.makedirs(args.out_dir, exist_ok=True)
     if args.raw:
         args.raw = os.path.abspath(args.raw)
         os.makedirs(args.raw, exist_ok=True)
-    {"counters": counters, "kernels": kernel_times, "trace": trace}[args.what](args)
+    {"counters": counters, "kernels": kernel_times, "trace": trace, "expert": expert}[args.what](args)
 
 
 if __name__ == "__main__":
