@@ -5,7 +5,9 @@ of ``libmoe_token_block.so``.  PyTorch provides device memory and the stream;
 each call runs on the input tensor's device and that device's current stream
 (P1, commit messages: launch stream, allocations and the stochastic-rounding
 state follow the input tensor's device).  There is no CPU fallback: if the
-library is missing, every entry point raises.
+library is missing, every entry point raises.  No call records an autograd
+graph: results do not require a gradient whatever the inputs do, and gradients
+are calls of their own.
 """
 
 import ctypes

@@ -109,7 +109,8 @@ __device__ __forceinline__ int slot_row(const int32_t* __restrict__ dst_row, con
 // same in every lane, so its slots are scalars, and the loads of KU slots go
 // out before the first is used (one slot at a time, with a wave per block and
 // 2-byte loads, took 1072 us at 16384 x 7168, top-8).  Bound by memory: 2115 MB
-// in 357 us are 5.9 TB/s, where a large copy reaches 5.0.
+// in 357 us are 5.9 TB/s; a copy of 1 GiB by the same 16-byte streamed accesses
+// reaches 6.5, a read alone 7.1.
 template <int KU, bool STREAM, typename IDX>
 __global__ __launch_bounds__(256) void k_bf16_combine(const uint16_t* __restrict__ rows, int r_cap, int H, int k,
                                                       int segs, int waves, const int32_t* __restrict__ dst_row,
@@ -155,7 +156,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 // its slots then follow one another).  A lane keeps NP pieces of dout for all
 // the token's slots, so dout is read once; the loads of KU slots go out
 // together.  Each lane sums its own products, then the lanes and the four waves
-// in a fixed order.  Bound by memory: 1345 MB in 242 us, 5.6 TB/s.
+// in a fixed order.  Bound by memory: 1345 MB in 244 us, 5.5 TB/s.
 template <int NP, int KU, bool STREAM>
 __global__ __launch_bounds__(256) void k_bf16_combine_bwd(const uint16_t* __restrict__ dout,
                                                           const uint16_t* __restrict__ rows, int T, int H, int k,

@@ -179,14 +179,15 @@ __device__ __forceinline__ void clear_unnamed(const IDX* __restrict__ ids, int i
 // (a power of two, whole rounds of the WK waves), rows padded by 16 bytes so that
 // the 16 entries of a read lie in different banks.
 //
-// 8 tokens, top-8 of 32 experts, 7168 x 2048: 60 us for 232 MB (3.9 TB/s); one
+// 8 tokens, top-8 of 32 experts, 7168 x 2048: 61 us for 232 MB (3.8 TB/s); one
 // token, top-8 of 32, 4096 x 7168 with SwiGLU: 30 us for 132 MB (4.4 TB/s); the
 // same weights by a wave per output and entry: 133 us for the first.  What is left
 // above the copy rate is a block's first loads, which the few blocks of such a
 // call do not hide, and lines fetched twice: rows of 9 K / 16 + 4 bytes end
 // inside 128-byte lines, and a line that two steps share has often left the L2
-// in between (31% more lines than the weights have; reading further ahead makes
-// it more).
+// in between (331 MB come past the L2 in the first call, 43% more than its bytes,
+// at 5.5 TB/s; 718 for 530 MB at 32 tokens, top-8 of 32, 4096 x 7168; reading
+// further ahead makes it more).
 template <int RT, int WN, bool SWIGLU, typename IDX>
 __global__ __launch_bounds__(512) void k_nvfp4_matvec(const uint16_t* __restrict__ x, int K, int x_div,
                                                       const uint8_t* __restrict__ weight, int E, int N,
@@ -348,8 +349,10 @@ __global__ __launch_bounds__(512) void k_nvfp4_matvec(const uint16_t* __restrict
 // way in registers, and so are the next step's weights, issued after it, so that
 // neither wait includes the other.
 //
-// 128 tokens, top-8 of 32, 4096 x 7168 with SwiGLU: 172 us, 3.1 TB/s of weights
-// and 349 TFLOP/s; passes of 16 entries, which read the weights again for every
+// 128 tokens, top-8 of 32, 4096 x 7168 with SwiGLU: 169 to 183 us from process to
+// process, 3.2 to 2.9 TB/s of its 535 MB (849 come past the L2, up to 5.0 TB/s) and
+// 355 to 328 TFLOP/s; VALU instructions issue 46% of the time, the matrix unit is
+// busy 18%; passes of 16 entries, which read the weights again for every
 // 16, take 309.  Alone, the reads take 89 us and the decoding and products 104:
 // the two waves of a SIMD, in step with their blocks' barriers, overlap them only
 // in part.  Measured without gain: weights two and three steps ahead (they share
@@ -532,10 +535,15 @@ MTB_EXPORT int32_t ep_nvfp4_expert_matvec(const uint16_t* x, int64_t tokens, int
   hipStream_t s = (hipStream_t)stream;
   const int NO = swiglu ? N / 2 : N;
   constexpr int RT = 2;
-  // From 16 entries an expert on, the wide kernel, if its blocks reach every CU.
-  // 4096 x 7168 with SwiGLU, 32 experts: 16 entries each 144 us against 190; 12:
-  // 145, 141; 8: 140, 126; 7168 x 2048: 12: 85, 80; 8: 83, 71.  128 entries of one
-  // 7168 x 7168 matrix would be 56 of its blocks and 119 us, against 47.
+  // From 16 entries an expert on (on average), the wide kernel, if its blocks reach
+  // every CU: the narrow one reads an expert's weights again for every 16 entries.
+  // Wide and narrow, 32 experts, top-8, by the mean of uniform routing: 4096 x 7168
+  // with SwiGLU, 16: 152, 185 us; 15: 150, 179; 14: 151, 172; 13: 148, 162; 12: 146,
+  // 145; 8: 142, 127; 7168 x 2048, 16: 88, 99; 14: 86, 91; 13: 86, 87; 12: 85, 81;
+  // 8: 83, 74.  So the two cross between 12 and 13, and means of 13 to 16 are
+  // served up to a fifth slower than they could be.  Skewed ids (exponent 1.2) at 12:
+  // 146, 157 and 84, 88.  128 entries of one 7168 x 7168 matrix would be 56 of the
+  // wide kernel's blocks and 119 us, against 47.
   const int wide_cols = (swiglu ? 32 : 64) * RT, wide_blocks = (NO + wide_cols - 1) / wide_cols * E;
   if (M >= 16 * E && wide_blocks >= 256) {
     constexpr int NT = 4;
