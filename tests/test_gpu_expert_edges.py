@@ -1,6 +1,7 @@
 """The expert layer's calls at their edges on the GPU: empty batches, weights of
 unused slots that are not numbers, pre-activations that are not finite, small
-weights times large activations.  Bounds are those of ``test_gpu_expert``."""
+weights times large activations, one plan in a captured graph, no autograd graph.
+Bounds are those of ``test_gpu_expert``."""
 
 import os
 import sys
@@ -193,3 +194,52 @@ def test_matvec_of_small_weights_and_large_activations(dev, t, e, n, k, scale, x
     y, _ = expert.matvec(expert.f64(xb), w, ids)
     assert np.abs(y).max() < 2.0 ** 127
     _check_matvec(got, expert.f64(xb), w, ids, False, f"scale {scale}")
+
+
+# ------------------------------------------------------------------ graphs, autograd
+def test_serving_in_a_graph_follows_its_ids(dev):
+    # one plan for every step: what a replay drops are the slots that its ids leave unused
+    torch.manual_seed(4)
+    t, h, f, e, k = 6, 256, 64, 8, 2
+    layer = ex.ExpertLayer(e, h, f, dev, seed=2)
+    packed, entries = layer.pack(), mtb.ep_entry_plan(t, k, dev)
+    x = torch.randn(t, h, device=dev).bfloat16()
+    ids = torch.zeros((t, k), dtype=torch.int32, device=dev)
+    w = torch.zeros((t, k), device=dev)
+
+    def step(drop):
+        top = torch.topk(torch.randn(t, e, device=dev), k)
+        unused = torch.rand(t, k, device=dev) < drop
+        ids.copy_(top.indices.int().masked_fill(unused, -1))
+        w.copy_(torch.softmax(top.values, 1).masked_fill(unused, float("nan")))
+        x.copy_(torch.randn(t, h, device=dev).bfloat16())
+
+    step(0.0)
+    side = torch.cuda.Stream(dev)
+    side.wait_stream(torch.cuda.current_stream(dev))
+    with torch.cuda.stream(side):
+        ex.serve(x, ids, w, packed, entries)
+    torch.cuda.current_stream(dev).wait_stream(side)
+    torch.cuda.synchronize(dev)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = ex.serve(x, ids, w, packed, entries)
+    for i, drop in enumerate((0.0, 0.5, 1.0, 0.2)):
+        step(drop)
+        g.replay()
+        torch.cuda.synchronize(dev)
+        assert_bytes_equal(host(out), host(ex.serve(x, ids, w, packed, entries)), f"replay {i}")
+        assert bool(torch.isfinite(out.float()).all()) and not host(out)[host((ids < 0).all(1))].any()
+
+
+def test_results_carry_no_autograd_graph(dev):
+    x = torch.randn(4, 128, device=dev).bfloat16().requires_grad_(True)
+    w = torch.rand(4, 2, device=dev).requires_grad_(True)
+    ids = torch.zeros((4, 2), dtype=torch.int32, device=dev)
+    plan = mtb.ep_route_plan(ids, 2)
+    rows = mtb.ep_bf16_dispatch(x, plan)
+    act, data, scales = mtb.swiglu_mxfp8_checkpoint(x)
+    weight = mtb.ep_nvfp4_pack(torch.randn(8, 128, device=dev).bfloat16()).view(2, 4, -1)
+    results = [rows, mtb.ep_bf16_combine(rows, plan, w), *mtb.ep_bf16_combine_bwd(x, rows, plan, w), act,
+               mtb.ep_nvfp4_expert_matvec(x, weight, ids), *mtb.dswiglu_mxfp8_checkpoint(data, scales, act)]
+    assert not any(r.requires_grad for r in results)
