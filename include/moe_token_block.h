@@ -83,6 +83,10 @@ enum ep_status {
 #define EP_IDX_INT32 0
 #define EP_IDX_INT64 1
 
+/* row formats of ep_mxfp4_grouped_gemm */
+#define EP_ROWS_MXFP4 0
+#define EP_ROWS_MXFP8 1
+
 /* ---------------------------------------------------------------- helpers */
 
 /* ABI version of the loaded library (EP_ABI_VERSION it was built with). */
@@ -577,6 +581,94 @@ int32_t swiglu_mxfp8_checkpoint(const uint16_t* preact, int64_t tokens, int64_t 
  *   for swiglu_mxfp8_checkpoint. */
 int32_t dswiglu_mxfp8_checkpoint(const uint8_t* data, const uint8_t* scales, const uint16_t* dy, int64_t tokens,
                                  int64_t ffn, uint16_t* dx, uint16_t* act, void* stream);
+
+/* ---------------------------------------------------------------- products of grouped rows */
+
+/* The products of grouped BF16 rows with their experts' weights, and both
+ * gradients.  counts [E] and offsets [E+1] are a routing plan's: expert e's grouped
+ * rows are [offsets[e], offsets[e+1]), the first counts[e] of which hold entries.
+ * Both NULL: one dense matrix (num_experts 1), every row below r_cap an entry.
+ * entries: an upper bound of the sum of counts (tokens * top_k of the plan, or
+ * r_cap); it picks the kernel and no result depends on it.  Spans taken from
+ * counts and offsets are kept within [0, r_cap).
+ *   ep_bf16_grouped_gemm:  out[g, n] = sum_k rows[g, k] weight[e, n, k]
+ *   ep_bf16_grouped_dgrad: drows[g, k] = sum_n dout[g, n] weight[e, n, k]
+ *   ep_bf16_grouped_wgrad: dweight[e, n, k] = sum_g dout[g, n] rows[g, k]
+ * rows and drows [r_cap, hidden], dout and out [r_cap, width], weight [E, width,
+ * hidden] BF16; dweight [E, width, hidden] BF16 or (f32 != 0) FP32.  Sums are FP32
+ * in an order fixed by the sizes and the plan, rounded once.  Grouped rows that hold
+ * no entry are not used; the first two write every row below r_cap that
+ * the plan's spans cover or that lies behind them, zeros where there is no entry,
+ * and the third writes every expert's weights, zeros for one without entries.
+ *   hidden and width from 1 to 2^20, 1 <= num_experts <= 1024, r_cap < 2^25, and at
+ *   most 2^31 tiles (EP_ERR_RANGE); no row needs an alignment.
+ *   workspace of ep_bf16_grouped_wgrad_workspace_bytes(...) bytes, 16-byte aligned
+ *   (EP_ERR_WORKSPACE; NULL where that is 0). */
+int32_t ep_bf16_grouped_gemm(const uint16_t* rows, int64_t r_cap, int64_t hidden, const uint16_t* weight,
+                             int64_t num_experts, int64_t width, const int32_t* counts, const int32_t* offsets,
+                             int64_t entries, uint16_t* out, void* stream);
+int32_t ep_bf16_grouped_dgrad(const uint16_t* dout, int64_t r_cap, int64_t width, const uint16_t* weight,
+                              int64_t num_experts, int64_t hidden, const int32_t* counts, const int32_t* offsets,
+                              int64_t entries, uint16_t* drows, void* stream);
+size_t ep_bf16_grouped_wgrad_workspace_bytes(int64_t width, int64_t hidden, int64_t num_experts, int64_t entries);
+int32_t ep_bf16_grouped_wgrad(const uint16_t* dout, const uint16_t* rows, int64_t r_cap, int64_t width, int64_t hidden,
+                              int64_t num_experts, const int32_t* counts, const int32_t* offsets, int64_t entries,
+                              void* dweight, int32_t f32, void* workspace, size_t workspace_bytes, void* stream);
+
+/* BF16 rows to MXFP4: per 32 values the least e with max|x| <= 6 * 2^e within
+ * [-127, 127] (0 for a block of zeros), scale byte e + 127, codes E2M1 nearest even
+ * of x / 2^e; the layout of ep_mxfp4_direct_receive's rowwise operand, codes
+ * [rows, hidden/2] and scales [rows, hidden/32].  A block with an infinity or a NaN
+ * gets scale byte 255: all of it reads back as NaN.  ep_mxfp4_unpack: the values as
+ * BF16, rounded once (exact but at its ends).
+ *   Requires hidden a positive multiple of 32, at most 2^24; rows * hidden < 2^40. */
+int32_t ep_mxfp4_pack(const uint16_t* x, int64_t rows, int64_t hidden, uint8_t* codes, uint8_t* scales, void* stream);
+int32_t ep_mxfp4_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t hidden, uint16_t* out,
+                        void* stream);
+
+/* Grouped MXFP4 or MXFP8 rows times MXFP4 weights,
+ *   out[g, n] = sum_k a[g, k] weight[e, n, k], a and weight the values that codes and
+ *   scales stand for, BF16 [r_cap, width].
+ *   row_format EP_ROWS_MXFP4: data [r_cap, hidden/2], the rowwise operand of
+ *   ep_mxfp4_direct_receive; EP_ROWS_MXFP8: data [r_cap, hidden], as
+ *   ep_mxfp8_direct_receive writes it; scales [r_cap, hidden/32].  weight_codes [E,
+ *   width, hidden/2], weight_scales [E, width, hidden/32]: ep_mxfp4_pack's of the
+ *   weights.  Groups, entries, rows without entries and limits as for
+ *   ep_bf16_grouped_gemm; hidden a multiple of 32.
+ * Sums are FP32 in an order fixed by the sizes.  Products of MXFP4 rows are exact;
+ * of MXFP8 rows, the matrix instruction adds eight neighbouring products at a time
+ * (values 8i .. 8i+7), each cut at 2^-13 of the largest of the eight. */
+int32_t ep_mxfp4_grouped_gemm(const uint8_t* data, const uint8_t* scales, int32_t row_format, int64_t r_cap,
+                              int64_t hidden, const uint8_t* weight_codes, const uint8_t* weight_scales,
+                              int64_t num_experts, int64_t width, const int32_t* counts, const int32_t* offsets,
+                              int64_t entries, uint16_t* out, void* stream);
+
+/* ---------------------------------------------------------------- norm */
+
+/* The root-mean-square norm in front of an expert layer, with the residual's
+ * addition before it and an MXFP8 output (the rows that ep_mxfp8_direct_receive
+ * takes):
+ *   h = bf16(x + residual) (residual NULL: h = x, and h is not written)
+ *   rstd[t] = 1 / sqrt(mean(h[t]^2) + eps), y = h * rstd * weight, in FP32
+ *   data, scales = MXFP8 of y as in ep_mxfp8_pack, from FP32 with one rounding; a
+ *   block of 32 with an infinity or a NaN gets scale byte 255
+ *   x, residual, h [rows, hidden] and weight [hidden] BF16, data [rows, hidden],
+ *   scales [rows, hidden/32], rstd [rows] FP32.  Requires hidden a positive multiple
+ *   of 32, at most 16384; rows < 2^30; eps from 2^-100 to 1e30; FP32 has to hold the sum of a row's
+ *   squares.  h may be x or residual (the same address).
+ * drmsnorm: with g = weight * dy,
+ *   dx = rstd * (g - h * rstd^2 * mean(g * h)) + dh, rounded once to BF16 (dh NULL:
+ *   nothing added): the gradient of x and of residual, dh being h's own from the
+ *   residual path; dweight = sum over rows of dy * h * rstd, FP32 [hidden], zeros for
+ *   no rows, in an order fixed by the sizes.
+ *   workspace: drmsnorm_workspace_bytes(rows, hidden) bytes, 16-byte aligned
+ *   (EP_ERR_WORKSPACE; NULL with no rows). */
+int32_t rmsnorm_mxfp8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t rows, int64_t hidden,
+                      float eps, uint16_t* h, uint8_t* data, uint8_t* scales, float* rstd, void* stream);
+size_t drmsnorm_workspace_bytes(int64_t rows, int64_t hidden);
+int32_t drmsnorm(const uint16_t* dy, const uint16_t* h, const uint16_t* weight, const float* rstd, const uint16_t* dh,
+                 int64_t rows, int64_t hidden, uint16_t* dx, float* dweight, void* workspace, size_t workspace_bytes,
+                 void* stream);
 
 #ifdef __cplusplus
 }

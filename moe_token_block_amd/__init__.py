@@ -16,5 +16,8 @@ from .binding import (  # noqa: F401
     dswiglu_nvfp4_quant_noalloc, EP_NOALLOC_SCRATCH_BYTES, EP_ERR_SCRATCH,
     ep_mxfp8_unpack, ep_bf16_dispatch, ep_bf16_combine, ep_bf16_combine_bwd, ep_entry_plan, ep_nvfp4_expert_matvec,
     swiglu_mxfp8_checkpoint, dswiglu_mxfp8_checkpoint,
+    ep_bf16_grouped_gemm, ep_bf16_grouped_dgrad, ep_bf16_grouped_wgrad, ep_bf16_grouped_wgrad_workspace_bytes,
+    ep_mxfp4_pack, ep_mxfp4_unpack, ep_mxfp4_grouped_gemm, EP_ROWS_MXFP4, EP_ROWS_MXFP8,
+    rmsnorm_mxfp8, drmsnorm, drmsnorm_workspace_bytes,
     lib, LIB_PATH, EXPORTS,
 )

@@ -22,6 +22,7 @@ LIB_PATH = os.path.join(_HERE, "libmoe_token_block.so")
 EP_ROUND_NEAREST, EP_ROUND_SR_ELEMENT, EP_ROUND_SR_STREAM = 0, 1, 2
 EP_ROUND_SR_ELEMENT_CARRY, EP_ROUND_SR_STREAM_CARRY = 3, 4
 EP_IDX_INT32, EP_IDX_INT64 = 0, 1
+EP_ROWS_MXFP4, EP_ROWS_MXFP8 = 0, 1
 EP_DEVERR_EXPERT_ID = 1
 EP_ERR_SCRATCH = -9
 EP_NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -68,6 +69,16 @@ _SIGS = {
     "ep_nvfp4_expert_matvec": (_I32, [_P, _I64, _I64, _I32, _P, _I64, _I64, _P, _I32, _I64, _I32, _P, _P, _P]),
     "swiglu_mxfp8_checkpoint": (_I32, [_P, _I64, _I64, _P, _P, _P, _P]),
     "dswiglu_mxfp8_checkpoint": (_I32, [_P, _P, _P, _I64, _I64, _P, _P, _P]),
+    "ep_bf16_grouped_gemm": (_I32, [_P, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _P, _P]),
+    "ep_bf16_grouped_dgrad": (_I32, [_P, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _P, _P]),
+    "ep_bf16_grouped_wgrad_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64]),
+    "ep_bf16_grouped_wgrad": (_I32, [_P, _P, _I64, _I64, _I64, _I64, _P, _P, _I64, _P, _I32, _P, _SZ, _P]),
+    "ep_mxfp4_pack": (_I32, [_P, _I64, _I64, _P, _P, _P]),
+    "ep_mxfp4_unpack": (_I32, [_P, _P, _I64, _I64, _P, _P]),
+    "ep_mxfp4_grouped_gemm": (_I32, [_P, _P, _I32, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _P, _P]),
+    "rmsnorm_mxfp8": (_I32, [_P, _P, _P, _I64, _I64, ctypes.c_float, _P, _P, _P, _P, _P]),
+    "drmsnorm_workspace_bytes": (_SZ, [_I64, _I64]),
+    "drmsnorm": (_I32, [_P, _P, _P, _P, _P, _I64, _I64, _P, _P, _P, _SZ, _P]),
     "dswiglu_nvfp4_quant": (_I32, [_P, _P, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "dswiglu_nvfp4_quant_sr": (_I32, [_P, _P, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P]),
     "dswiglu_nvfp4_quant_sr_stream": (_I32, [_P, _P, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P,
@@ -812,6 +823,246 @@ def dswiglu_mxfp8_checkpoint(data, scales, dy, dx=None, act=None, need_act=True)
     _launch(index, "dswiglu_mxfp8_checkpoint", data.data_ptr(), scales.data_ptr(), dy.data_ptr(), t, f2 // 2,
             dx.data_ptr(), None if act is None else act.data_ptr())
     return dx, act
+
+
+# ------------------------------------------------------------------ products of grouped rows
+def _groups(plan, index, rows, experts):
+    """counts and offsets of a plan and an upper bound of its entries, for ``rows``
+    grouped rows and ``experts`` weights; without a plan one dense matrix."""
+    if plan is None:
+        return None, None, rows
+    counts, offsets = plan["counts"], plan["offsets"]
+    if int(plan["r_cap"]) != rows:
+        raise ValueError(f"the plan has {int(plan['r_cap'])} grouped rows, the input {rows}")
+    _want(counts, _I32T, "plan counts", index, (experts,))
+    _want(offsets, _I32T, "plan offsets", index, (experts + 1,))
+    return counts.data_ptr(), offsets.data_ptr(), plan["dst_row"].numel()
+
+
+def _weights(weight, plan, name):
+    """Experts, width and last size of weights [E, N, K], or [N, K] without a plan."""
+    if weight.dim() != (2 if plan is None else 3):
+        raise ValueError(f"{name} must be " + ("[width, hidden] without a plan" if plan is None else
+                                               "[experts, width, hidden] with a plan"))
+    return (1 if plan is None else weight.shape[0]), weight.shape[-2], weight.shape[-1]
+
+
+def ep_bf16_grouped_gemm(rows, weight, plan=None, out=None):
+    """Each expert's grouped rows times its weights: out[g] = weight[e] @ rows[g], BF16
+    [r_cap, N] of rows BF16 [r_cap, K] and weight BF16 [E, N, K] (FP32 sums, rounded
+    once).  Rows that hold no entry are not used and come out as zeros.  Without a
+    plan: rows [M, K] times one matrix [N, K]."""
+    index, k = _index(rows), _width(rows, "rows")
+    e, n, wk = _weights(weight, plan, "weight")
+    r = rows.shape[0]
+    counts, offsets, entries = _groups(plan, index, r, e)
+    _want(rows, _BF16, "rows", index, (r, wk))
+    _want(weight, _BF16, "weight", index, weight.shape)
+    if out is None:
+        out = rows.new_empty((r, n))
+    else:
+        _want(out, _BF16, "out", index, (r, n))
+    _launch(index, "ep_bf16_grouped_gemm", rows.data_ptr(), r, k, weight.data_ptr(), e, n, counts, offsets, entries,
+            out.data_ptr())
+    return out
+
+
+def ep_bf16_grouped_dgrad(dout, weight, plan=None, out=None):
+    """The gradient of ``ep_bf16_grouped_gemm`` by its rows: weight[e]^T @ dout[g], BF16
+    [r_cap, K] of dout BF16 [r_cap, N]; zeros where there is no entry."""
+    index, n = _index(dout), _width(dout, "dout")
+    e, wn, k = _weights(weight, plan, "weight")
+    r = dout.shape[0]
+    counts, offsets, entries = _groups(plan, index, r, e)
+    _want(dout, _BF16, "dout", index, (r, wn))
+    _want(weight, _BF16, "weight", index, weight.shape)
+    if out is None:
+        out = dout.new_empty((r, k))
+    else:
+        _want(out, _BF16, "out", index, (r, k))
+    _launch(index, "ep_bf16_grouped_dgrad", dout.data_ptr(), r, n, weight.data_ptr(), e, k, counts, offsets, entries,
+            out.data_ptr())
+    return out
+
+
+def ep_bf16_grouped_wgrad(dout, rows, plan=None, out=None, dtype=torch.bfloat16, workspace=None):
+    """The gradient of ``ep_bf16_grouped_gemm`` by its weights: the sum of dout[g] rows[g]^T
+    over each expert's entries, [E, N, K] (without a plan [N, K]) in BF16 or, with
+    ``dtype=torch.float32``, FP32; zeros for an expert without entries.  ``workspace``:
+    uint8 of ``ep_bf16_grouped_wgrad_workspace_bytes``, allocated if None."""
+    index, n, k = _index(dout), _width(dout, "dout"), _width(rows, "rows")
+    r = dout.shape[0]
+    e = 1 if plan is None else int(plan["num_experts"])
+    counts, offsets, entries = _groups(plan, index, r, e)
+    _want(dout, _BF16, "dout", index, (r, n))
+    _want(rows, _BF16, "rows", index, (r, k))
+    shape = (n, k) if plan is None else (e, n, k)
+    if out is None:
+        if dtype not in (_BF16, _F32):
+            raise TypeError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
+        out = dout.new_empty(shape, dtype=dtype)
+    else:
+        _want(out, _F32 if out.dtype is _F32 else _BF16, "out", index, shape)
+    wsb = lib().ep_bf16_grouped_wgrad_workspace_bytes(n, k, e, entries)
+    if workspace is None:
+        workspace = dout.new_empty(wsb, dtype=_U8) if wsb else None
+    else:
+        _need(workspace, _U8, "workspace", dout.device, numel=wsb)
+    _launch(index, "ep_bf16_grouped_wgrad", dout.data_ptr(), rows.data_ptr(), r, n, k, e, counts, offsets, entries,
+            out.data_ptr(), int(out.dtype is _F32), None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel())
+    return out
+
+
+def ep_bf16_grouped_wgrad_workspace_bytes(width, hidden, num_experts, entries):
+    """Workspace of ``ep_bf16_grouped_wgrad`` for a plan of ``entries`` = tokens * top_k."""
+    return lib().ep_bf16_grouped_wgrad_workspace_bytes(width, hidden, num_experts, entries)
+
+
+def ep_mxfp4_pack(x, codes=None, scales=None):
+    """BF16 rows [T, H] -> MXFP4 (codes uint8 [T, H/2], even element in the low nibble;
+    E8M0 scales uint8 [T, H/32]); H a multiple of 32.  A block of 32 that is not finite
+    reads back as NaN.  Weights [E, N, K] are packed as [E * N, K] rows."""
+    index, h = _index(x), _width(x, "x")
+    if h % 32:
+        raise ValueError("x must be [rows, hidden] with hidden a multiple of 32")
+    t = x.shape[0]
+    _want(x, _BF16, "x", index, (t, h))
+    if codes is None:
+        codes = x.new_empty((t, h // 2), dtype=_U8)
+    else:
+        _want(codes, _U8, "codes", index, (t, h // 2))
+    if scales is None:
+        scales = x.new_empty((t, h // 32), dtype=_U8)
+    else:
+        _want(scales, _U8, "scales", index, (t, h // 32))
+    _launch(index, "ep_mxfp4_pack", x.data_ptr(), t, h, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def _mxfp4(codes, scales, index, what):
+    """Checks MXFP4 tensors [.., K/2] and [.., K/32]; returns K."""
+    h = 2 * codes.shape[-1] if codes.dim() else 0
+    if h % 32:
+        raise ValueError(f"{what} codes must be [.., hidden/2] with hidden a multiple of 32")
+    _want(codes, _U8, f"{what} codes", index, codes.shape)
+    _want(scales, _U8, f"{what} scales", index, codes.shape[:-1] + (h // 32,))
+    return h
+
+
+def ep_mxfp4_unpack(codes, scales, out=None):
+    """MXFP4 rows (codes uint8 [T, H/2], scales uint8 [T, H/32]) -> BF16 [T, H]."""
+    index = _index(codes)
+    t, h = codes.shape[0], 2 * _width(codes, "codes")
+    _mxfp4(codes, scales, index, "MXFP4")
+    if out is None:
+        out = codes.new_empty((t, h), dtype=_BF16)
+    else:
+        _want(out, _BF16, "out", index, (t, h))
+    _launch(index, "ep_mxfp4_unpack", codes.data_ptr(), scales.data_ptr(), t, h, out.data_ptr())
+    return out
+
+
+def ep_mxfp4_grouped_gemm(data, scales, weight_codes, weight_scales, plan=None, out=None):
+    """Grouped MXFP4 or MXFP8 rows times their experts' MXFP4 weights: BF16 [r_cap, N],
+    FP32 sums, rounded once; rows that hold no entry are not used and come out as zeros.
+    ``data`` uint8 [r_cap, K/2]: MXFP4 rows (``ep_mxfp4_direct_receive``'s rowwise operand,
+    or ``ep_mxfp4_pack``'s); [r_cap, K]: MXFP8 rows (``ep_mxfp8_direct_receive``'s);
+    ``scales`` uint8 [r_cap, K/32].  Weights: ``ep_mxfp4_pack``'s, viewed [E, N, K/2] and
+    [E, N, K/32].  Without a plan: one matrix of weights [N, K/2]."""
+    index, b = _index(data), _width(data, "data")
+    e, n, _ = _weights(weight_codes, plan, "weight_codes")
+    h = _mxfp4(weight_codes, weight_scales, index, "weight")
+    r = data.shape[0]
+    counts, offsets, entries = _groups(plan, index, r, e)
+    if b != h and 2 * b != h:
+        raise ValueError(f"data has {b} bytes a row: {h // 2} (MXFP4) or {h} (MXFP8) go with weights of {h} columns")
+    _want(data, _U8, "data", index, (r, b))
+    _want(scales, _U8, "scales", index, (r, h // 32))
+    if out is None:
+        out = data.new_empty((r, n), dtype=_BF16)
+    else:
+        _want(out, _BF16, "out", index, (r, n))
+    _launch(index, "ep_mxfp4_grouped_gemm", data.data_ptr(), scales.data_ptr(), EP_ROWS_MXFP8 if b == h else EP_ROWS_MXFP4,
+            r, h, weight_codes.data_ptr(), weight_scales.data_ptr(), e, n, counts, offsets, entries, out.data_ptr())
+    return out
+
+
+# ------------------------------------------------------------------ norm
+def rmsnorm_mxfp8(x, weight, residual=None, eps=1e-6, h=None, data=None, scales=None, rstd=None):
+    """The norm in front of an expert layer with an MXFP8 output: of h = BF16(x +
+    residual), y = h * rstd * weight, quantized from FP32: (data uint8 [T, H], scales
+    uint8 [T, H/32], h BF16 [T, H], rstd float32 [T]).  Without a residual h is x itself.
+    ``h`` may be x or residual (the sum in place).  H: a multiple of 32 up to 16384;
+    eps from 2^-100 to 1e30."""
+    index, hid = _index(x), _width(x, "x")
+    if hid % 32:
+        raise ValueError("x must be [tokens, hidden] with hidden a multiple of 32")
+    t = x.shape[0]
+    _want(x, _BF16, "x", index, (t, hid))
+    _want(weight, _BF16, "weight", index, (hid,))
+    if residual is None:
+        if h is not None and h is not x:
+            raise ValueError("h is written only with a residual")
+        h, rp = x, None
+    else:
+        _want(residual, _BF16, "residual", index, (t, hid))
+        rp = residual.data_ptr()
+        if h is None:
+            h = x.new_empty((t, hid))
+        else:
+            _want(h, _BF16, "h", index, (t, hid))
+    if data is None:
+        data = x.new_empty((t, hid), dtype=_U8)
+    else:
+        _want(data, _U8, "data", index, (t, hid))
+    if scales is None:
+        scales = x.new_empty((t, hid // 32), dtype=_U8)
+    else:
+        _want(scales, _U8, "scales", index, (t, hid // 32))
+    if rstd is None:
+        rstd = x.new_empty((t,), dtype=_F32)
+    else:
+        _want(rstd, _F32, "rstd", index, (t,))
+    _launch(index, "rmsnorm_mxfp8", x.data_ptr(), rp, weight.data_ptr(), t, hid, eps, None if rp is None else h.data_ptr(),
+            data.data_ptr(), scales.data_ptr(), rstd.data_ptr())
+    return data, scales, h, rstd
+
+
+def drmsnorm(dy, h, weight, rstd, dh=None, dx=None, dweight=None, workspace=None):
+    """Gradients of ``rmsnorm_mxfp8`` for dy BF16 [T, H], from its h and rstd: (dx BF16
+    [T, H], the gradient of x and of the residual; dweight float32 [H]).  ``dh``: the
+    gradient that reaches h by the residual path, added to dx.  ``workspace``: uint8 of
+    ``drmsnorm_workspace_bytes(T, H)``, allocated if None."""
+    index, hid = _index(dy), _width(dy, "dy")
+    t = dy.shape[0]
+    _want(dy, _BF16, "dy", index, (t, hid))
+    _want(h, _BF16, "h", index, (t, hid))
+    _want(weight, _BF16, "weight", index, (hid,))
+    _want(rstd, _F32, "rstd", index, (t,))
+    if dh is not None:
+        _want(dh, _BF16, "dh", index, (t, hid))
+    if dx is None:
+        dx = dy.new_empty((t, hid))
+    else:
+        _want(dx, _BF16, "dx", index, (t, hid))
+    if dweight is None:
+        dweight = rstd.new_empty((hid,))
+    else:
+        _want(dweight, _F32, "dweight", index, (hid,))
+    wsb = lib().drmsnorm_workspace_bytes(t, hid)
+    if workspace is None:
+        workspace = rstd.new_empty(wsb, dtype=_U8)
+    else:
+        _need(workspace, _U8, "workspace", dy.device, numel=wsb)
+    _launch(index, "drmsnorm", dy.data_ptr(), h.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
+            None if dh is None else dh.data_ptr(), t, hid, dx.data_ptr(), dweight.data_ptr(), workspace.data_ptr(),
+            workspace.numel())
+    return dx, dweight
+
+
+def drmsnorm_workspace_bytes(rows, hidden):
+    return lib().drmsnorm_workspace_bytes(rows, hidden)
 
 
 # ------------------------------------------------------------------ dSwiGLU

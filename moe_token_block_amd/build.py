@@ -19,7 +19,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe_token_block.so")
 SOURCES = ["abi.hip", "pack.hip", "unpack.hip", "route.hip", "receive.hip", "dswiglu.hip", "consumer.hip",
-           "combine.hip", "matvec.hip", "swiglu.hip"]
+           "combine.hip", "matvec.hip", "swiglu.hip", "grouped.hip", "mxgemm.hip", "mxfp4.hip", "norm.hip"]
 ARCH = "gfx950"
 
 

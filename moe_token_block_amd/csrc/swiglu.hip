@@ -5,29 +5,12 @@
 #include "common.h"
 #include "launch.h"
 #include "mxfp8.h"
+#include "stream.h"
 
+// Every value here is read or written once: accesses past the caches (14841 x 2048:
+// the forward 45 -> 41 us, forward and read-back 72.2 -> 71.5, the gradient 54.7 ->
+// 50.0).
 namespace mtb {
-
-// Every value here is read or written once, and what is kept for the backward
-// pass is not read again soon: accesses past the caches, at any byte address
-// (14841 x 2048: the forward 45 -> 41 us, forward and read-back 72.2 -> 71.5, the
-// gradient 54.7 -> 50.0).
-template <typename T>
-__device__ __forceinline__ T ld_once(const void* p) {
-  typedef T any __attribute__((aligned(1)));
-  return __builtin_nontemporal_load(reinterpret_cast<const any*>(p));
-}
-template <typename T>
-__device__ __forceinline__ void st_once(void* p, T v) {
-  typedef T any __attribute__((aligned(1)));
-  __builtin_nontemporal_store(v, reinterpret_cast<any*>(p));
-}
-
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-// E8M0 byte -> the power of two it stands for (255: NaN).
-__device__ __forceinline__ float e8m0(uint32_t b) {
-  return b == 255u ? __uint_as_float(0x7FC00000u) : __builtin_ldexpf(1.0f, (int)b - 127);
-}
 
 // Eight E4M3 bytes times a power of two: exact in FP32.
 __device__ __forceinline__ void decode_e4m3x8(u32x2 v, float s, float* o) {
@@ -41,19 +24,9 @@ __device__ __forceinline__ void decode_e4m3x8(u32x2 v, float s, float* o) {
   o[7] = __builtin_amdgcn_cvt_f32_fp8((int)v.y, 3) * s;
 }
 
-__device__ __forceinline__ u32x4 pack8(const float* v) {
-  return u32x4{bf16pair(v[0], v[1]), bf16pair(v[2], v[3]), bf16pair(v[4], v[5]), bf16pair(v[6], v[7])};
-}
-
 __device__ __forceinline__ float silu(float a, float& s) {
   s = __builtin_amdgcn_rcpf(1.0f + __expf(-a));
   return a * s;
-}
-
-// The largest of a lane quad.
-__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));  // lane ^ 1
-  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));  // lane ^ 2
 }
 
 // Eight values of a 32-value block, whose largest magnitude is m, as E4M3 bytes;
