@@ -588,9 +588,9 @@ int32_t dswiglu_mxfp8_checkpoint(const uint8_t* data, const uint8_t* scales, con
  * gradients.  counts [E] and offsets [E+1] are a routing plan's: expert e's grouped
  * rows are [offsets[e], offsets[e+1]), the first counts[e] of which hold entries.
  * Both NULL: one dense matrix (num_experts 1), every row below r_cap an entry.
- * entries: an upper bound of the sum of counts (tokens * top_k of the plan, or
- * r_cap); it picks the kernel and no result depends on it.  Spans taken from
- * counts and offsets are kept within [0, r_cap).
+ * entries: at least the sum of counts (tokens * top_k of the plan, or r_cap); it
+ * picks the kernel and its launch.  Spans taken from counts and offsets are kept
+ * within [0, r_cap); those of different experts must not overlap.
  *   ep_bf16_grouped_gemm:  out[g, n] = sum_k rows[g, k] weight[e, n, k]
  *   ep_bf16_grouped_dgrad: drows[g, k] = sum_n dout[g, n] weight[e, n, k]
  *   ep_bf16_grouped_wgrad: dweight[e, n, k] = sum_g dout[g, n] rows[g, k]
@@ -601,7 +601,7 @@ int32_t dswiglu_mxfp8_checkpoint(const uint8_t* data, const uint8_t* scales, con
  * the plan's spans cover or that lies behind them, zeros where there is no entry,
  * and the third writes every expert's weights, zeros for one without entries.
  *   hidden and width from 1 to 2^20, 1 <= num_experts <= 1024, r_cap < 2^25, and at
- *   most 2^31 tiles (EP_ERR_RANGE); no row needs an alignment.
+ *   most 2^31 output tiles, entries < 2^31 (EP_ERR_RANGE); no row needs an alignment.
  *   workspace of ep_bf16_grouped_wgrad_workspace_bytes(...) bytes, 16-byte aligned
  *   (EP_ERR_WORKSPACE; NULL where that is 0). */
 int32_t ep_bf16_grouped_gemm(const uint16_t* rows, int64_t r_cap, int64_t hidden, const uint16_t* weight,
@@ -662,7 +662,7 @@ int32_t ep_mxfp4_grouped_gemm(const uint8_t* data, const uint8_t* scales, int32_
  *   residual path; dweight = sum over rows of dy * h * rstd, FP32 [hidden], zeros for
  *   no rows, in an order fixed by the sizes.
  *   workspace: drmsnorm_workspace_bytes(rows, hidden) bytes, 16-byte aligned
- *   (EP_ERR_WORKSPACE; NULL with no rows). */
+ *   (EP_ERR_WORKSPACE; NULL where that is 0). */
 int32_t rmsnorm_mxfp8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t rows, int64_t hidden,
                       float eps, uint16_t* h, uint8_t* data, uint8_t* scales, float* rstd, void* stream);
 size_t drmsnorm_workspace_bytes(int64_t rows, int64_t hidden);

@@ -161,6 +161,13 @@ def _want(t, dtype, name, index, shape):
         _need(t, dtype, name, torch.device("cuda", index), shape=shape)
 
 
+def _flat(t, dtype, name, index):
+    """Refuses (as ``_need``) a tensor that is not a contiguous ``dtype`` one on GPU
+    ``index``, whatever its shape."""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == index and t.is_contiguous()):
+        _need(t, dtype, name, torch.device("cuda", index))
+
+
 def _dev(t):
     if not t.is_cuda:
         raise ValueError("tensors must live on a GPU (no CPU path)")
@@ -832,19 +839,51 @@ def _groups(plan, index, rows, experts):
     if plan is None:
         return None, None, rows
     counts, offsets = plan["counts"], plan["offsets"]
-    if int(plan["r_cap"]) != rows:
-        raise ValueError(f"the plan has {int(plan['r_cap'])} grouped rows, the input {rows}")
-    _want(counts, _I32T, "plan counts", index, (experts,))
-    _want(offsets, _I32T, "plan offsets", index, (experts + 1,))
+    _flat(counts, _I32T, "plan counts", index)
+    _flat(offsets, _I32T, "plan offsets", index)
+    if plan["r_cap"] != rows or counts.numel() != experts or offsets.numel() != experts + 1:
+        raise ValueError(f"the plan has {plan['r_cap']} grouped rows, {counts.numel()} counts and {offsets.numel()} offsets; "
+                         f"{rows} rows and {experts} experts were handed over")
     return counts.data_ptr(), offsets.data_ptr(), plan["dst_row"].numel()
 
 
 def _weights(weight, plan, name):
     """Experts, width and last size of weights [E, N, K], or [N, K] without a plan."""
-    if weight.dim() != (2 if plan is None else 3):
-        raise ValueError(f"{name} must be " + ("[width, hidden] without a plan" if plan is None else
-                                               "[experts, width, hidden] with a plan"))
-    return (1 if plan is None else weight.shape[0]), weight.shape[-2], weight.shape[-1]
+    shape = weight.shape
+    if plan is None:
+        if len(shape) == 2:
+            return 1, shape[0], shape[1]
+    elif len(shape) == 3:
+        return shape
+    raise ValueError(f"{name} must be " + ("[width, hidden] without a plan" if plan is None else
+                                           "[experts, width, hidden] with a plan"))
+
+
+def _rows(t, name):
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be [rows, hidden]")
+    return shape
+
+
+def _product(name, x, weight, plan, out, across):
+    """The forward product and the rows' gradient, which differ in the weights' side
+    that x's columns meet."""
+    index = _index(x)
+    r, have = _rows(x, "dout" if across else "rows")
+    e, n, k = _weights(weight, plan, "weight")
+    terms, cols = (n, k) if across else (k, n)
+    if have != terms:
+        raise ValueError(f"rows of {have} values do not go with weights {tuple(weight.shape)}")
+    counts, offsets, entries = _groups(plan, index, r, e)
+    _flat(x, _BF16, "dout" if across else "rows", index)
+    _flat(weight, _BF16, "weight", index)
+    if out is None:
+        out = x.new_empty((r, cols))
+    else:
+        _want(out, _BF16, "out", index, (r, cols))
+    _launch(index, name, x.data_ptr(), r, terms, weight.data_ptr(), e, cols, counts, offsets, entries, out.data_ptr())
+    return out
 
 
 def ep_bf16_grouped_gemm(rows, weight, plan=None, out=None):
@@ -852,37 +891,13 @@ def ep_bf16_grouped_gemm(rows, weight, plan=None, out=None):
     [r_cap, N] of rows BF16 [r_cap, K] and weight BF16 [E, N, K] (FP32 sums, rounded
     once).  Rows that hold no entry are not used and come out as zeros.  Without a
     plan: rows [M, K] times one matrix [N, K]."""
-    index, k = _index(rows), _width(rows, "rows")
-    e, n, wk = _weights(weight, plan, "weight")
-    r = rows.shape[0]
-    counts, offsets, entries = _groups(plan, index, r, e)
-    _want(rows, _BF16, "rows", index, (r, wk))
-    _want(weight, _BF16, "weight", index, weight.shape)
-    if out is None:
-        out = rows.new_empty((r, n))
-    else:
-        _want(out, _BF16, "out", index, (r, n))
-    _launch(index, "ep_bf16_grouped_gemm", rows.data_ptr(), r, k, weight.data_ptr(), e, n, counts, offsets, entries,
-            out.data_ptr())
-    return out
+    return _product("ep_bf16_grouped_gemm", rows, weight, plan, out, False)
 
 
 def ep_bf16_grouped_dgrad(dout, weight, plan=None, out=None):
     """The gradient of ``ep_bf16_grouped_gemm`` by its rows: weight[e]^T @ dout[g], BF16
     [r_cap, K] of dout BF16 [r_cap, N]; zeros where there is no entry."""
-    index, n = _index(dout), _width(dout, "dout")
-    e, wn, k = _weights(weight, plan, "weight")
-    r = dout.shape[0]
-    counts, offsets, entries = _groups(plan, index, r, e)
-    _want(dout, _BF16, "dout", index, (r, wn))
-    _want(weight, _BF16, "weight", index, weight.shape)
-    if out is None:
-        out = dout.new_empty((r, k))
-    else:
-        _want(out, _BF16, "out", index, (r, k))
-    _launch(index, "ep_bf16_grouped_dgrad", dout.data_ptr(), r, n, weight.data_ptr(), e, k, counts, offsets, entries,
-            out.data_ptr())
-    return out
+    return _product("ep_bf16_grouped_dgrad", dout, weight, plan, out, True)
 
 
 def ep_bf16_grouped_wgrad(dout, rows, plan=None, out=None, dtype=torch.bfloat16, workspace=None):
@@ -890,27 +905,30 @@ def ep_bf16_grouped_wgrad(dout, rows, plan=None, out=None, dtype=torch.bfloat16,
     over each expert's entries, [E, N, K] (without a plan [N, K]) in BF16 or, with
     ``dtype=torch.float32``, FP32; zeros for an expert without entries.  ``workspace``:
     uint8 of ``ep_bf16_grouped_wgrad_workspace_bytes``, allocated if None."""
-    index, n, k = _index(dout), _width(dout, "dout"), _width(rows, "rows")
-    r = dout.shape[0]
-    e = 1 if plan is None else int(plan["num_experts"])
+    index = _index(dout)
+    (r, n), (m, k) = _rows(dout, "dout"), _rows(rows, "rows")
+    if m != r:
+        raise ValueError(f"dout has {r} rows, rows {m}")
+    e = 1 if plan is None else plan["num_experts"]
     counts, offsets, entries = _groups(plan, index, r, e)
-    _want(dout, _BF16, "dout", index, (r, n))
-    _want(rows, _BF16, "rows", index, (r, k))
+    _flat(dout, _BF16, "dout", index)
+    _flat(rows, _BF16, "rows", index)
     shape = (n, k) if plan is None else (e, n, k)
     if out is None:
         if dtype not in (_BF16, _F32):
             raise TypeError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
         out = dout.new_empty(shape, dtype=dtype)
     else:
-        _want(out, _F32 if out.dtype is _F32 else _BF16, "out", index, shape)
-    wsb = lib().ep_bf16_grouped_wgrad_workspace_bytes(n, k, e, entries)
-    if workspace is None:
-        workspace = dout.new_empty(wsb, dtype=_U8) if wsb else None
-    else:
+        dtype = _F32 if out.dtype is _F32 else _BF16
+        _want(out, dtype, "out", index, shape)
+    wsb = (_lib or lib()).ep_bf16_grouped_wgrad_workspace_bytes(n, k, e, entries)
+    if workspace is not None:
         _need(workspace, _U8, "workspace", dout.device, numel=wsb)
+        wsb = workspace.numel()
+    elif wsb:
+        workspace = dout.new_empty(wsb, dtype=_U8)
     _launch(index, "ep_bf16_grouped_wgrad", dout.data_ptr(), rows.data_ptr(), r, n, k, e, counts, offsets, entries,
-            out.data_ptr(), int(out.dtype is _F32), None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel())
+            out.data_ptr(), dtype is _F32, None if workspace is None else workspace.data_ptr(), wsb)
     return out
 
 
@@ -940,26 +958,19 @@ def ep_mxfp4_pack(x, codes=None, scales=None):
     return codes, scales
 
 
-def _mxfp4(codes, scales, index, what):
-    """Checks MXFP4 tensors [.., K/2] and [.., K/32]; returns K."""
-    h = 2 * codes.shape[-1] if codes.dim() else 0
-    if h % 32:
-        raise ValueError(f"{what} codes must be [.., hidden/2] with hidden a multiple of 32")
-    _want(codes, _U8, f"{what} codes", index, codes.shape)
-    _want(scales, _U8, f"{what} scales", index, codes.shape[:-1] + (h // 32,))
-    return h
-
-
 def ep_mxfp4_unpack(codes, scales, out=None):
     """MXFP4 rows (codes uint8 [T, H/2], scales uint8 [T, H/32]) -> BF16 [T, H]."""
     index = _index(codes)
-    t, h = codes.shape[0], 2 * _width(codes, "codes")
-    _mxfp4(codes, scales, index, "MXFP4")
+    t, b = _rows(codes, "codes")
+    if b % 16:
+        raise ValueError("codes must be [rows, hidden/2] with hidden a multiple of 32")
+    _flat(codes, _U8, "codes", index)
+    _want(scales, _U8, "scales", index, (t, b // 16))
     if out is None:
-        out = codes.new_empty((t, h), dtype=_BF16)
+        out = codes.new_empty((t, 2 * b), dtype=_BF16)
     else:
-        _want(out, _BF16, "out", index, (t, h))
-    _launch(index, "ep_mxfp4_unpack", codes.data_ptr(), scales.data_ptr(), t, h, out.data_ptr())
+        _want(out, _BF16, "out", index, (t, 2 * b))
+    _launch(index, "ep_mxfp4_unpack", codes.data_ptr(), scales.data_ptr(), t, 2 * b, out.data_ptr())
     return out
 
 
@@ -970,15 +981,18 @@ def ep_mxfp4_grouped_gemm(data, scales, weight_codes, weight_scales, plan=None, 
     or ``ep_mxfp4_pack``'s); [r_cap, K]: MXFP8 rows (``ep_mxfp8_direct_receive``'s);
     ``scales`` uint8 [r_cap, K/32].  Weights: ``ep_mxfp4_pack``'s, viewed [E, N, K/2] and
     [E, N, K/32].  Without a plan: one matrix of weights [N, K/2]."""
-    index, b = _index(data), _width(data, "data")
-    e, n, _ = _weights(weight_codes, plan, "weight_codes")
-    h = _mxfp4(weight_codes, weight_scales, index, "weight")
-    r = data.shape[0]
+    index = _index(data)
+    r, b = _rows(data, "data")
+    e, n, half = _weights(weight_codes, plan, "weight_codes")
+    h, blocks = 2 * half, half // 16
+    if half % 16 or (b != half and b != h):
+        raise ValueError(f"data of {b} bytes a row do not go with weight codes {tuple(weight_codes.shape)}: hidden a multiple "
+                         f"of 32, hidden/2 bytes (MXFP4) or hidden (MXFP8)")
     counts, offsets, entries = _groups(plan, index, r, e)
-    if b != h and 2 * b != h:
-        raise ValueError(f"data has {b} bytes a row: {h // 2} (MXFP4) or {h} (MXFP8) go with weights of {h} columns")
-    _want(data, _U8, "data", index, (r, b))
-    _want(scales, _U8, "scales", index, (r, h // 32))
+    _flat(data, _U8, "data", index)
+    _want(scales, _U8, "scales", index, (r, blocks))
+    _flat(weight_codes, _U8, "weight_codes", index)
+    _want(weight_scales, _U8, "weight_scales", index, (n, blocks) if plan is None else (e, n, blocks))
     if out is None:
         out = data.new_empty((r, n), dtype=_BF16)
     else:
@@ -1050,14 +1064,15 @@ def drmsnorm(dy, h, weight, rstd, dh=None, dx=None, dweight=None, workspace=None
         dweight = rstd.new_empty((hid,))
     else:
         _want(dweight, _F32, "dweight", index, (hid,))
-    wsb = lib().drmsnorm_workspace_bytes(t, hid)
-    if workspace is None:
-        workspace = rstd.new_empty(wsb, dtype=_U8)
-    else:
+    wsb = (_lib or lib()).drmsnorm_workspace_bytes(t, hid)
+    if workspace is not None:
         _need(workspace, _U8, "workspace", dy.device, numel=wsb)
+        wsb = workspace.numel()
+    elif wsb:
+        workspace = rstd.new_empty(wsb, dtype=_U8)
     _launch(index, "drmsnorm", dy.data_ptr(), h.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
-            None if dh is None else dh.data_ptr(), t, hid, dx.data_ptr(), dweight.data_ptr(), workspace.data_ptr(),
-            workspace.numel())
+            None if dh is None else dh.data_ptr(), t, hid, dx.data_ptr(), dweight.data_ptr(),
+            None if workspace is None else workspace.data_ptr(), wsb)
     return dx, dweight
 
 

@@ -3,11 +3,10 @@
 #pragma once
 
 #include "common.h"
+#include "quad.h"
 
 namespace mtb {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // The grouped rows as a routing plan has them: expert e's are [offsets[e],
@@ -20,53 +19,75 @@ struct Groups {
   int experts, r_cap;
 };
 
-// A stretch of at most `rows` grouped rows from row0 on, all of one expert: the
-// first `used` of its `extent` rows hold entries, the others get zeros.
+// A stretch of an expert's rows from row0 on, of which the first `used` (at most a
+// tile's) hold entries: the rest of its `extent`, which may be more than a tile's,
+// gets zeros.
 struct Span {
   int expert, row0, used, extent;
 };
 
-// The t-th of the tiles of BM rows that cover every expert's rows and then those
-// behind the last expert's; `total` of them.  All lanes of a wave call it
-// together; the scan over the experts costs about the latency of two loads.
-template <int BM>
-__device__ __forceinline__ bool find_span(const Groups& gr, int tiles_n, Span& s, int& tile_n, int GM) {
-  const int lane = threadIdx.x & 63;
-  const int nb = gr.counts ? gr.experts + 1 : 1;
-  int total = 0;
-  // how many tiles there are
-  for (int base = 0; base < nb; base += 64) {
-    const int e = base + lane;
-    int tiles = 0;
-    if (e < nb) {
-      const int lo = gr.counts ? min(max(gr.offsets[e], 0), gr.r_cap) : 0;
-      const int hi = gr.counts && e < gr.experts ? min(max(gr.offsets[e + 1], lo), gr.r_cap) : gr.r_cap;
-      tiles = (hi - lo + BM - 1) / BM;
+constexpr int kTailRows = 256;  // rows behind the last expert that one workgroup clears
+
+// Expert e's rows (e == experts: those behind the last expert's) and its tiles of BM.
+__device__ __forceinline__ void group_rows(const Groups& gr, int e, int BM, int& lo, int& hi, int& cnt, int& tiles) {
+  lo = hi = cnt = tiles = 0;
+  if (!gr.counts) {
+    if (e == 0) {
+      hi = cnt = gr.r_cap;
+      tiles = (cnt + BM - 1) / BM;
     }
+  } else if (e < gr.experts) {
+    lo = min(max(gr.offsets[e], 0), gr.r_cap);
+    hi = min(max(gr.offsets[e + 1], lo), gr.r_cap);
+    cnt = min(max(gr.counts[e], 0), hi - lo);
+    tiles = hi > lo ? max((cnt + BM - 1) / BM, 1) : 0;
+  } else if (e == gr.experts) {
+    lo = min(max(gr.offsets[e], 0), gr.r_cap);
+    hi = gr.r_cap;
+    tiles = (hi - lo + kTailRows - 1) / kTailRows;
+  }
+}
+
+// The id-th of tiles_m x tiles_n tiles in bands of eight rows by all columns.
+__device__ __forceinline__ void banded(int id, int tiles_m, int tiles_n, int& m, int& n) {
+  constexpr int kBand = 8;
+  const int band = id / (kBand * tiles_n), in = id - band * (kBand * tiles_n), rows = min(kBand, tiles_m - band * kBand);
+  m = band * kBand + in % rows;
+  n = in / rows;
+}
+
+// Workgroup `block`'s tile of tiles_m x tiles_n; false: none.  Neighbouring workgroups
+// lie on different XCDs: each of the eight takes a run of tiles of its own, so that
+// the tiles that run at once on one XCD share their operands in that XCD's L2.
+__device__ __forceinline__ bool tile_of(uint32_t block, int tiles_m, int tiles_n, int& m, int& n) {
+  const int all = tiles_m * tiles_n, chunk = (all + 7) >> 3;
+  const int at = (int)(block >> 3), id = (int)(block & 7) * chunk + at;
+  if (at >= chunk || id >= all) return false;
+  banded(id, tiles_m, tiles_n, m, n);
+  return true;
+}
+
+// The workgroup's tile of BM rows by one of tiles_n stretches of columns; false: none.
+// All lanes of a wave call it together; the scan over the experts costs about the
+// latency of two loads.
+template <int BM>
+__device__ __forceinline__ bool find_span(const Groups& gr, int tiles_n, Span& s, int& tile_n) {
+  const int lane = threadIdx.x & 63;
+  int total = 0;
+  for (int base = 0; base <= gr.experts; base += 64) {
+    int lo, hi, cnt, tiles;
+    group_rows(gr, base + lane, BM, lo, hi, cnt, tiles);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) tiles += __shfl_xor(tiles, o, 64);
     total += tiles;
   }
   total = __builtin_amdgcn_readfirstlane(total);
-  // Neighbouring workgroups lie on different XCDs: each of the eight takes a run of
-  // tiles of its own, GM rows of tiles by all columns at a time, so that what runs
-  // at once on one XCD shares its operands in that XCD's L2.
-  const int all = total * tiles_n, chunk = (all + 7) >> 3;
-  const int at = (int)(blockIdx.x >> 3), id = (int)(blockIdx.x & 7) * chunk + at;
-  if (at >= chunk || id >= all) return false;
-  const int band = id / (GM * tiles_n), in = id - band * (GM * tiles_n), gm = min(GM, total - band * GM);
-  int t = band * GM + in % gm;
-  tile_n = in / gm;
+  int t;
+  if (!tile_of(blockIdx.x, total, tiles_n, t, tile_n)) return false;
   // which expert the t-th belongs to
-  for (int base = 0;; base += 64) {
-    const int e = base + lane;
-    int tiles = 0, lo = 0, hi = 0, cnt = 0;
-    if (e < nb) {
-      lo = gr.counts ? min(max(gr.offsets[e], 0), gr.r_cap) : 0;
-      hi = gr.counts && e < gr.experts ? min(max(gr.offsets[e + 1], lo), gr.r_cap) : gr.r_cap;
-      cnt = gr.counts ? (e < gr.experts ? min(max(gr.counts[e], 0), hi - lo) : 0) : hi;
-      tiles = (hi - lo + BM - 1) / BM;
-    }
+  for (int base = 0; base <= gr.experts; base += 64) {
+    int lo, hi, cnt, tiles;
+    group_rows(gr, base + lane, BM, lo, hi, cnt, tiles);
     int upto = tiles;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -75,21 +96,25 @@ __device__ __forceinline__ bool find_span(const Groups& gr, int tiles_n, Span& s
     }
     const uint64_t past = __builtin_amdgcn_ballot_w64(upto > t);
     if (past) {
-      const int who = __builtin_ctzll(past);
-      const int first = (t - (__builtin_amdgcn_readlane(upto, who) - __builtin_amdgcn_readlane(tiles, who))) * BM;
+      const int who = __builtin_ctzll(past), n = __builtin_amdgcn_readlane(tiles, who);
+      const int i = t - (__builtin_amdgcn_readlane(upto, who) - n);
+      const int first = i * (base + who < gr.experts ? BM : kTailRows);
       s.expert = base + who;
       s.row0 = __builtin_amdgcn_readlane(lo, who) + first;
-      s.extent = min(__builtin_amdgcn_readlane(hi, who) - s.row0, BM);
-      s.used = min(max(__builtin_amdgcn_readlane(cnt, who) - first, 0), s.extent);
+      s.used = min(max(__builtin_amdgcn_readlane(cnt, who) - first, 0), BM);
+      const int rest = __builtin_amdgcn_readlane(hi, who) - s.row0;
+      s.extent = base + who == gr.experts ? min(rest, kTailRows) : i == n - 1 ? rest : BM;
       return true;
     }
     t -= __builtin_amdgcn_readlane(upto, 63);
   }
+  return false;
 }
 
-// Upper bound of find_span's workgroups for any plan (0 where it passes 2^31).
-inline int64_t span_blocks(int64_t r_cap, int64_t experts, bool dense, int bm, int64_t tiles_n) {
-  const int64_t tiles_m = dense ? (r_cap + bm - 1) / bm : r_cap / bm + experts + 1;
+// Upper bound of find_span's workgroups for any plan of so many entries.
+inline int64_t span_blocks(int64_t r_cap, int64_t experts, bool dense, int64_t entries, int bm, int64_t tiles_n) {
+  const int64_t most = entries < r_cap ? entries : r_cap;
+  const int64_t tiles_m = dense ? (r_cap + bm - 1) / bm : most / bm + experts + r_cap / kTailRows + 1;
   return (tiles_m * tiles_n + 7) / 8 * 8;
 }
 
@@ -138,6 +163,80 @@ __device__ __forceinline__ void store_block64(const f32x4 (&acc)[MT][4], char* l
     if (row >= used) v = u32x4{0u, 0u, 0u, 0u};
     if (row < rows && 8 * c < cols) store8(out + row * ld + 8 * c, v, cols - 8 * c);
   }
+}
+
+// The same in FP32, 16 rows at a time through 4096 bytes of LDS: sixteen lanes write a
+// row's 256 bytes.
+template <int MT>
+__device__ __forceinline__ void store_block64(const f32x4 (&acc)[MT][4], char* lds, float* out, int64_t ld, int rows,
+                                              int cols) {
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x4*>(lds + r * 256 + 16 * ((4 * i + g) ^ (r & 7))) = acc[j][i];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const int row = 4 * p + g, n = cols - 4 * r;
+      const f32x4 v = *reinterpret_cast<const f32x4*>(lds + row * 256 + 16 * (r ^ (row & 7)));
+      float* o = out + (16 * j + row) * ld + 4 * r;
+      if (16 * j + row >= rows) continue;
+      if (n >= 4) {
+        st_any<f32x4>(o, v);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (q < n) o[q] = v[q];
+      }
+    }
+  }
+}
+
+// Rows [first, rows) and columns [0, cols) of a tile: zeros.
+__device__ __forceinline__ void clear_rows(uint16_t* out, int64_t ld, int first, int rows, int cols) {
+  const int pieces = (cols + 7) >> 3;
+  for (int i = threadIdx.x; i < (rows - first) * pieces; i += blockDim.x)
+    store8(out + (int64_t)(first + i / pieces) * ld + 8 * (i % pieces), u32x4{0u, 0u, 0u, 0u}, cols - 8 * (i % pieces));
+}
+
+// The kernels for few rows: blockIdx.y is an expert or, past the last, a stretch of
+// the rows behind it.
+inline int64_t few_groups(int64_t r_cap, int64_t experts, bool dense) {
+  return dense ? 1 : experts + r_cap / kTailRows + 1;
+}
+// Its rows [lo, hi), the first cnt of which hold entries; false: none.
+__device__ __forceinline__ bool few_rows(const Groups& gr, int& lo, int& hi, int& cnt) {
+  const int e = blockIdx.y;
+  int tiles;
+  group_rows(gr, min(e, gr.experts), 16, lo, hi, cnt, tiles);
+  if (gr.counts && e >= gr.experts) {
+    lo += (e - gr.experts) * kTailRows;
+    hi = min(hi, lo + kTailRows);
+  }
+  return hi > lo;
+}
+
+// The waves' sums of 16 RT columns by 16 NT rows, added in the waves' order and stored
+// as BF16; lane (r, g) holds columns 16 i + 4 g .. + 3 of row 16 t + r in acc[t][i].
+// red: 1024 RT NT bytes a wave.
+template <int RT, int NT>
+__device__ __forceinline__ void join_few(const f32x4 (&acc)[NT][RT], float* red, uint16_t* out, int64_t ld, int used,
+                                         int cols) {
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, wave = threadIdx.x >> 6, W = blockDim.x >> 6;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+      *reinterpret_cast<f32x4*>(red + (((wave * NT + t) * RT + i) * 16 + r) * 16 + 4 * g) = acc[t][i];
+  __syncthreads();
+  for (int o = threadIdx.x; o < used * 16 * RT; o += blockDim.x) {
+    const int n = o % (16 * RT), m = o / (16 * RT);
+    const float* at = red + (((m >> 4) * RT + (n >> 4)) * 16 + (m & 15)) * 16 + (n & 15);
+    float y = 0.0f;
+    for (int v = 0; v < W; ++v) y += at[v * NT * RT * 256];
+    if (n < cols) out[m * ld + n] = __builtin_bit_cast(uint16_t, (__bf16)y);
+  }
+  __syncthreads();
 }
 
 }  // namespace mtb

@@ -19,49 +19,60 @@ constexpr int kBK = 64;  // terms of the sum in one step
 
 // An operand's tile: C output rows (or columns) by 64 terms, C * 128 bytes of LDS,
 // staged through registers by THREADS threads.
-template <int C, int THREADS, bool T>
+template <int C, int THREADS, bool T, int SETS>
 struct Tile {
   static constexpr int kPieces = C * 8 / THREADS;  // 16-byte pieces a thread
+  int tid;                                         // of the THREADS that share the tile
   uint32_t off[kPieces];                           // bytes from the step's base
-  u32x4 v[kPieces];
+  u32x4 v[SETS][kPieces];                          // of the steps whose loads are under way
 
   // ld: values from one row of the matrix to the next; c_n: rows (R) or columns (T)
   // that exist from the tile's first on, at least 1.
-  __device__ __forceinline__ void init(int64_t ld, int c_n) {
+  __device__ __forceinline__ void init(int thread, int64_t ld, int c_n) {
+    tid = thread;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int p = threadIdx.x + i * THREADS;
-      if (T) off[i] = (uint32_t)((p / (C / 8)) * (uint32_t)ld + 8 * (p % (C / 8))) * 2u;
+      const int p = tid + i * THREADS;
+      if (T) off[i] = (uint32_t)((p / (C / 8)) * (uint32_t)ld + 8 * min(p % (C / 8), (c_n - 1) >> 3)) * 2u;
       else off[i] = (uint32_t)(min(p >> 3, c_n - 1) * (uint32_t)ld + 8 * (p & 7)) * 2u;
     }
   }
-  // base: the step's first value; terms: how many of the step's 64 exist.  Rows (R)
-  // that do not exist repeat the last; columns (T) that do not, and terms, are zeros.
+  // base: the step's first value; terms: how many of the step's 64 exist.  Rows (R) that
+  // do not exist repeat the last, and pieces of columns (T) the last piece: what comes of
+  // them is not stored.  EDGE: terms that do not exist are zeros, and nothing past a
+  // row's last column is read (without it up to 7 values of the next row are).
   template <bool EDGE>
-  __device__ __forceinline__ void load(const uint16_t* base, int terms, int c_n) {
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const uint16_t* src = reinterpret_cast<const uint16_t*>(reinterpret_cast<const char*>(base) + off[i]);
-      const int p = threadIdx.x + i * THREADS;
-      if (!EDGE) v[i] = ld_any<u32x4>(src);
-      else if (T) v[i] = load8(src, p / (C / 8) < terms ? c_n - 8 * (p % (C / 8)) : 0);
-      else v[i] = load8(src, terms - 8 * (p & 7));
-    }
+  __device__ __forceinline__ void load_piece(int set, int i, const uint16_t* base, int terms, int c_n) {
+    const uint16_t* src = reinterpret_cast<const uint16_t*>(reinterpret_cast<const char*>(base) + off[i]);
+    const int p = tid + i * THREADS;
+    if (!EDGE) v[set][i] = ld_any<u32x4>(src);
+    else if (T) v[set][i] = load8(src, p / (C / 8) < terms ? c_n - 8 * (p % (C / 8)) : 0);
+    else v[set][i] = load8(src, terms - 8 * (p & 7));
   }
-  __device__ __forceinline__ void store(char* lds) const {
+  template <bool EDGE>
+  __device__ __forceinline__ void load(int set, const uint16_t* base, int terms, int c_n) {
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int p = threadIdx.x + i * THREADS;
-      uint32_t at;
-      if (T) {
-        const int k = p / (C / 8), c = p % (C / 8);
-        at = k * (2 * C) + 16 * (c ^ (2 * (k & 3)));
-      } else {
-        const int row = p >> 3, c = p & 7;
-        at = row * 128 + 16 * (c ^ (row & 7));
-      }
-      *reinterpret_cast<u32x4*>(lds + at) = v[i];
+    for (int i = 0; i < kPieces; ++i) load_piece<EDGE>(set, i, base, terms, c_n);
+  }
+  // T: the 32 lanes of half a transposing read take 32 bytes of each of eight rows
+  // (four terms of two lane groups): the rows' 32-byte pieces are permuted so that
+  // they meet every bank once.
+  static __device__ __forceinline__ int key(int k) { return (k & 3) + (C >= 128 ? 4 * ((k >> 3) & 1) : 0); }
+  __device__ __forceinline__ void store_piece(int set, int i, char* lds) const {
+    const int p = tid + i * THREADS;
+    uint32_t at;
+    if (T) {
+      const int k = p / (C / 8), c = p % (C / 8);
+      at = k * (2 * C) + 16 * (c ^ (2 * key(k)));
+    } else {
+      const int row = p >> 3, c = p & 7;
+      at = row * 128 + 16 * (c ^ (row & 7));
     }
+    *reinterpret_cast<u32x4*>(lds + at) = v[set][i];
+  }
+  __device__ __forceinline__ void store(int set, char* lds) const {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) store_piece(set, i, lds);
   }
   // The instruction's operand of the 16 output rows (columns) from c0 on and the 32
   // terms from 32 ks on: lane (r, g) holds terms 8 g .. 8 g + 7 of c0 + r.
@@ -71,7 +82,7 @@ struct Tile {
       typedef short i16x4 __attribute__((ext_vector_type(4)));
       typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
       const int k = 32 * ks + 8 * g + (r >> 2);  // this lane's row of the four that are transposed
-      const uint32_t at = k * (2 * C) + ((2 * c0 + 8 * (r & 3)) ^ (32 * (k & 3)));
+      const uint32_t at = k * (2 * C) + ((2 * c0 + 8 * (r & 3)) ^ (32 * key(k)));
       i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(lds + at));
       i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(lds + at + 8 * C));
       typedef short i16x8 __attribute__((ext_vector_type(8)));
@@ -82,83 +93,164 @@ struct Tile {
   }
 };
 
-// acc += P Q^T over `terms` terms: P (BM output rows) and Q (BN output columns) with
-// first values p and q, and rows p_ld and q_ld values apart.
-template <int BM, int BN, int WM, int WN, bool PT, bool QT>
+// acc = P Q^T over `terms` terms: P (BM output rows) and Q (BN output columns) with
+// first values p and q, and rows p_ld and q_ld values apart.  SETS steps' loads are
+// under way beside the step that LDS holds next.  SHARES groups of WM x WN waves take
+// the steps in turn, each through buffers of its own; the first ends with the sum.
+template <int BM, int BN, int WM, int WN, bool PT, bool QT, int SETS, int SHARES>
 struct Product {
   static constexpr int kThreads = 64 * WM * WN, MT = BM / WM / 16, NT = BN / WN / 16;
-  static constexpr int kBuf = (BM + BN) * 128, kLds = 2 * kBuf;
+  typedef Tile<BM, kThreads, PT, SETS> TileP;
+  typedef Tile<BN, kThreads, QT, SETS> TileQ;
+  static_assert(TileP::kPieces + TileQ::kPieces == 8, "a piece for each of a step's eight parts");
+  
+  static constexpr bool GROUPED = !PT && !QT && BM == 256;
+  static constexpr int kBuf = (BM + BN) * 128, kLds = 2 * SHARES * kBuf;
   f32x4 acc[MT][NT];
 
-  __device__ __forceinline__ void run(char* lds, const uint16_t* p, int64_t p_ld, int p_n, const uint16_t* q,
+  // A step's products in eight parts, `between(part)` called in each.  GROUP: a part's
+  // reads, store, load and products are kept together (131072 rows, 7168 x 4096: 7.00 ->
+  // 6.84 ms; where an operand is read across, or with small tiles, it costs 2 to 20%).
+  template <bool GROUP, typename F>
+  __device__ __forceinline__ void compute(const char* buf, int wm, int wn, F&& between) {
+    bf16x8 b[NT];
+    static_for<0, 8>([&](auto part) {
+      constexpr int c = decltype(part)::value, ks = c / 4, jg = c % 4, J = MT / 4;
+      if constexpr (jg == 0) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) b[i] = TileQ::frag(buf + BM * 128, 16 * (wn * NT + i), ks);
+      }
+      between(part);
+#pragma unroll
+      for (int j = jg * J; j < (jg + 1) * J; ++j) {
+        const bf16x8 a = TileP::frag(buf, 16 * (wm * MT + j), ks);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[i], a, acc[j][i], 0, 0, 0);
+      }
+      if constexpr (GROUP) {
+        __builtin_amdgcn_sched_group_barrier(0x100, J + (jg == 0 ? (QT ? 2 : 1) * NT : 0), 0);
+        __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x8, NT * J, 0);
+      }
+    });
+  }
+
+  __device__ __forceinline__ void run(char* all_lds, const uint16_t* p, int64_t p_ld, int p_n, const uint16_t* q,
                                       int64_t q_ld, int q_n, int terms) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave / WN, wn = wave % WN;
+    const int share = SHARES == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
+    const int tid = threadIdx.x - share * kThreads;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
+    char* lds = all_lds + share * 2 * kBuf;
 #pragma unroll
     for (int j = 0; j < MT; ++j)
 #pragma unroll
       for (int i = 0; i < NT; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if (terms <= 0) return;
-    Tile<BM, kThreads, PT> tp;
-    Tile<BN, kThreads, QT> tq;
-    tp.init(p_ld, p_n);
-    tq.init(q_ld, q_n);
+    TileP tp;
+    TileQ tq;
+    tp.init(tid, p_ld, p_n);
+    tq.init(tid, q_ld, q_n);
     const int64_t p_step = PT ? kBK * p_ld : kBK, q_step = QT ? kBK * q_ld : kBK;
-    const bool p_cut = PT && p_n < BM, q_cut = QT && q_n < BN;
-    int left = terms;  // terms that are not loaded yet
-    auto load = [&]() {
-      if (left >= kBK && !p_cut) tp.template load<false>(p, left, p_n);
-      else tp.template load<true>(p, left, p_n);
-      if (left >= kBK && !q_cut) tq.template load<false>(q, left, q_n);
-      else tq.template load<true>(q, left, q_n);
-      p += p_step;
-      q += q_step;
-      left -= kBK;
+    const bool p_cut = PT && p_n < BM && p_n % 8, q_cut = QT && q_n < BN && q_n % 8;
+    p += share * p_step;
+    q += share * q_step;
+    int left = terms - share * kBK;  // from this group's next step on: terms that are not loaded yet
+    const int all = (terms + kBK - 1) / kBK, steps = (all + SHARES - 1) / SHARES;
+    const int mine = (all - share + SHARES - 1) / SHARES;  // steps of this group; the first has `steps`
+    auto advance = [&]() {
+      p += SHARES * p_step;
+      q += SHARES * q_step;
+      left -= SHARES * kBK;
     };
-    auto compute = [&](const char* buf) {
-      const char* qb = buf + BM * 128;
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        bf16x8 a[MT], b[NT];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) b[i] = Tile<BN, kThreads, QT>::frag(qb, 16 * (wn * NT + i), ks);
-#pragma unroll
-        for (int j = 0; j < MT; ++j) a[j] = Tile<BM, kThreads, PT>::frag(buf, 16 * (wm * MT + j), ks);
+    auto load = [&](int set) {
+      if (left <= 0) return;
+      if (left >= kBK && !p_cut) tp.template load<false>(set, p, left, p_n);
+      else tp.template load<true>(set, p, left, p_n);
+      if (left >= kBK && !q_cut) tq.template load<false>(set, q, left, q_n);
+      else tq.template load<true>(set, q, left, q_n);
+      advance();
+    };
+    load(0);
+    if (mine > 0) {
+      tp.store(0, lds);
+      tq.store(0, lds + BM * 128);
+    }
+    static_for<0, SETS>([&](auto set) { load(set); });  // set i: the step 1 + i
+    __syncthreads();
+    // The steps whose loads (1 + SETS steps ahead) are whole: one run of instructions,
+    // the next step's values on their way to LDS and a later one's to the registers
+    // they leave, a piece at a time between the products.
+    int t = 0;
+    // the same for both groups; without the last where a row's end is read past
+    const int whole = terms / kBK / SHARES - 1 - SETS - (p_cut || q_cut ? 1 : 0);
+    for (; t + SETS <= whole; t += SETS) {
+      static_for<0, SETS>([&](auto sub) {
+        constexpr int set = decltype(sub)::value;
+        const char* cur = lds + (((t + set) & 1) ? kBuf : 0);
+        char* next = lds + (((t + set) & 1) ? 0 : kBuf);
+        compute<GROUPED>(cur, wm, wn, [&](auto part) {
+          constexpr int c = decltype(part)::value;
+          if constexpr (c < TileP::kPieces) {
+            tp.store_piece(set, c, next);
+            tp.template load_piece<false>(set, c, p, kBK, p_n);
+          } else {
+            tq.store_piece(set, c - TileP::kPieces, next + BM * 128);
+            tq.template load_piece<false>(set, c - TileP::kPieces, q, kBK, q_n);
+          }
+        });
+        advance();
+        __syncthreads();
+      });
+    }
+    for (; t < steps; t += SETS) {
+      static_for<0, SETS>([&](auto sub) {
+        constexpr int set = decltype(sub)::value;
+        if (t + set >= steps) return;
+        const char* cur = lds + (((t + set) & 1) ? kBuf : 0);
+        char* next = lds + (((t + set) & 1) ? 0 : kBuf);
+        if (t + set + 1 < mine) {
+          tp.store(set, next);
+          tq.store(set, next + BM * 128);
+          load(set);
+        }
+        if (t + set < mine) compute<false>(cur, wm, wn, [](auto) {});
+        __syncthreads();
+      });
+    }
+    if constexpr (SHARES == 2) {  // the buffers are free: the second group's sums to the first
+      static_assert(kLds >= BM * BN * 4, "the sums fit the buffers");
+      f32x4* at = reinterpret_cast<f32x4*>(all_lds) + tid * MT * NT;
+      const int turn = tid & 7;  // a lane's pieces in another order for each of eight: no bank is met twice
+      if (share) {
 #pragma unroll
         for (int j = 0; j < MT; ++j)
 #pragma unroll
-          for (int i = 0; i < NT; ++i) acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[i], a[j], acc[j][i], 0, 0, 0);
+          for (int i = 0; i < NT; ++i) at[(j * NT + i) ^ turn] = acc[j][i];
       }
-    };
-    load();
-    tp.store(lds);
-    tq.store(lds + BM * 128);
-    if (left > 0) load();
-    const int steps = (terms + kBK - 1) / kBK;
-    __syncthreads();
-    for (int t = 0; t < steps; ++t) {
-      char* next = lds + ((t & 1) ? 0 : kBuf);
-      if (t + 1 < steps) {  // the next step's values, loaded a step ago, to the other buffer
-        tp.store(next);
-        tq.store(next + BM * 128);
-        if (left > 0) load();
+      __syncthreads();
+      if (!share) {
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int i = 0; i < NT; ++i) acc[j][i] += at[(j * NT + i) ^ turn];
       }
-      compute(lds + ((t & 1) ? kBuf : 0));
       __syncthreads();
     }
   }
 };
 
 // out[m, n] for grouped rows m: P the rows, Q the weights (QT: their transposes).
-template <int BM, int BN, int WM, int WN, bool QT>
-__global__ __launch_bounds__(64 * WM * WN) void k_bf16_grouped_gemm(const uint16_t* __restrict__ rows, int64_t K,
+template <int BM, int BN, int WM, int WN, int SETS, int SHARES, bool QT>
+__global__ __launch_bounds__(64 * WM * WN * SHARES) void k_bf16_grouped_gemm(const uint16_t* __restrict__ rows, int64_t K,
                                                                     const uint16_t* __restrict__ weight, int64_t N,
                                                                     Groups gr, uint16_t* __restrict__ out) {
-  typedef Product<BM, BN, WM, WN, false, QT> P;
+  typedef Product<BM, BN, WM, WN, false, QT, SETS, SHARES> P;
   extern __shared__ char lds[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave / WN, wn = wave % WN;
   Span s;
   int tn;
-  if (!find_span<BM>(gr, (int)((N + BN - 1) / BN), s, tn, 8)) return;
+  if (!find_span<BM>(gr, (int)((N + BN - 1) / BN), s, tn)) return;
   P prod;
   const int n0 = tn * BN;
   const int64_t ld = QT ? N : K;  // values of a weight row; K terms, N columns
@@ -169,50 +261,238 @@ __global__ __launch_bounds__(64 * WM * WN) void k_bf16_grouped_gemm(const uint16
     prod.run(lds, rows, K, 1, weight, ld, 1, 0);
   }
   static_assert(P::NT == 4, "a wave stores 64 columns");
+  if (s.extent > BM)
+    clear_rows(out + (int64_t)s.row0 * N + n0, N, BM, s.extent, (int)min((int64_t)BN, N - n0));
+  if (wave >= WM * WN) return;
   const int m = wm * P::MT * 16, n = n0 + wn * 64;
   store_block64<P::MT>(prod.acc, lds + wave * P::MT * 2048, out + (int64_t)(s.row0 + m) * N + n, N, s.used - m,
                        s.extent - m, (int)min((int64_t)64, N - n));
 }
 
-// dW of one expert: P dout's columns, Q the rows' columns, the sum over the expert's rows.
-template <int BM, int BN, int WM, int WN, bool F32>
-__global__ __launch_bounds__(64 * WM * WN) void k_bf16_grouped_wgrad(const uint16_t* __restrict__ dout, int64_t N,
+// out[m, n] for experts with few rows, where the time is that of reading the weights.
+// A workgroup takes 16 RT weight rows of one expert and 16 NT of its rows at a time (the
+// z-th of gridDim.z first, then every gridDim.z-th); its waves take the sum's steps of 128 terms in turn and join their sums
+// through LDS.  Weights and rows go from memory to registers, four lanes on 64
+// contiguous bytes, and are brought into the instruction's order within lane quads;
+// a step's loads are in flight while the step before is multiplied.
+template <int RT, int NT>
+__global__ __launch_bounds__(NT == 1 ? 512 : 256) void k_bf16_grouped_few(const uint16_t* __restrict__ rows, int64_t K,
+                                                          const uint16_t* __restrict__ weight, int64_t N, Groups gr,
+                                                          uint16_t* __restrict__ out) {
+  extern __shared__ char lds[];
+  float* red = reinterpret_cast<float*>(lds);  // [waves][RT * NT][16 rows][16 columns]
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), W = blockDim.x >> 6;
+  const int n0 = (int)blockIdx.x * 16 * RT, cols = (int)min((int64_t)16 * RT, N - n0);
+  const int e = blockIdx.y;
+  int lo, hi, cnt;
+  if (!few_rows(gr, lo, hi, cnt)) return;
+  if (blockIdx.z == 0) clear_rows(out + (int64_t)lo * N + n0, N, cnt, hi - lo, cols);
+
+  // lane 16 g + 4 b + c loads, for j = 0..3, chunk 4 g + c (8 terms) of row 4 b + j; the
+  // quad's exchange leaves chunk 4 g + j of row 4 b + c in register j
+  const int g = lane >> 4, b4 = lane & 12, k0 = 8 * (4 * g + (lane & 3));
+  const uint16_t* w = weight + ((int64_t)e * N + n0) * K + k0;
+  uint32_t woff[RT][4];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) woff[i][j] = (uint32_t)min(16 * i + b4 + j, cols - 1) * (uint32_t)K;
+  const int steps = (int)((K + 127) / 128);
+  struct Step {
+    u32x4 w[RT][4], x[NT][4];
+  };
+  for (int c0 = 16 * NT * (int)blockIdx.z; c0 < cnt; c0 += 16 * NT * (int)gridDim.z) {
+    const int used = min(cnt - c0, 16 * NT);
+    const uint16_t* x = rows + (int64_t)(lo + c0) * K + k0;
+    uint32_t xoff[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) xoff[i][j] = (uint32_t)min(16 * i + b4 + j, used - 1) * (uint32_t)K;
+    f32x4 acc[NT][RT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < RT; ++i) acc[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto load = [&](int s, Step& d) {
+      const int at = s * 128, left = (int)min((int64_t)K - at - k0, (int64_t)8);
+      if ((int64_t)at + 128 <= K) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+          for (int i = 0; i < RT; ++i) d.w[i][j] = ld_any<u32x4>(w + woff[i][j] + at);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) d.x[i][j] = ld_any<u32x4>(x + xoff[i][j] + at);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+          for (int i = 0; i < RT; ++i) d.w[i][j] = load8(w + woff[i][j] + at, left);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) d.x[i][j] = load8(x + xoff[i][j] + at, left);
+        }
+      }
+    };
+    auto multiply = [&](Step& d) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i) quad_transpose(d.w[i]);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) quad_transpose(d.x[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < RT; ++i)
+            acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, d.w[i][j]),
+                                                                __builtin_bit_cast(bf16x8, d.x[t][j]), acc[t][i], 0, 0, 0);
+    };
+    Step s0, s1;
+    int s = wave;
+    if (s < steps) load(s, s0);
+    for (; s < steps; s += 2 * W) {
+      if (s + W < steps) load(s + W, s1);
+      multiply(s0);
+      if (s + 2 * W < steps) load(s + 2 * W, s0);
+      if (s + W < steps) multiply(s1);
+    }
+    join_few<RT, NT>(acc, red, out + (int64_t)(lo + c0) * N + n0, N, used, cols);
+  }
+}
+
+// drows for experts with few rows: as k_bf16_grouped_few, but the weights' rows are the
+// sum's terms: a wave's 64 of them by 64 columns go through LDS of its own, whose
+// transposing read makes the instruction's operand.
+template <int NT>
+__global__ __launch_bounds__(512) void k_bf16_grouped_few_across(const uint16_t* __restrict__ dout, int64_t N,
+                                                                 const uint16_t* __restrict__ weight, int64_t K,
+                                                                 Groups gr, uint16_t* __restrict__ drows) {
+  extern __shared__ char lds[];  // 8 KB a wave; at the end [waves][4 * NT][16 rows][16 columns] floats
+  typedef Tile<64, 64, true, 1> TileQ;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), W = blockDim.x >> 6;
+  const int k0 = (int)blockIdx.x * 64, cols = (int)min((int64_t)64, K - k0), e = blockIdx.y;
+  int lo, hi, cnt;
+  if (!few_rows(gr, lo, hi, cnt)) return;
+  if (blockIdx.z == 0) clear_rows(drows + (int64_t)lo * K + k0, K, cnt, hi - lo, cols);
+  const int r = lane & 15, g = lane >> 4;
+  char* own = lds + wave * 8192;
+  const int steps = (int)((N + 63) / 64);
+  for (int c0 = 16 * NT * (int)blockIdx.z; c0 < cnt; c0 += 16 * NT * (int)gridDim.z) {
+    const int used = min(cnt - c0, 16 * NT);
+    const uint16_t* x = dout + (int64_t)(lo + c0) * N + 8 * g;
+    uint32_t xoff[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) xoff[t] = (uint32_t)min(16 * t + r, used - 1) * (uint32_t)N;
+    const uint16_t* w = weight + ((int64_t)e * N + 64 * wave) * K + k0;
+    f32x4 acc[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    struct Step {
+      TileQ q;
+      u32x4 x[NT][2];
+    };
+    Step s0, s1;
+    s0.q.init(lane, K, cols);
+    s1.q.init(lane, K, cols);
+    auto load = [&](int s, Step& d) {
+      const int left = (int)min(N - 64 * (int64_t)s, (int64_t)64);
+      if (left == 64 && cols == 64) d.q.template load<false>(0, w, 64, 64);
+      else d.q.template load<true>(0, w, left, cols);
+      w += 64 * (int64_t)W * K;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+          d.x[t][ks] = left == 64 ? ld_any<u32x4>(x + xoff[t] + 64 * s + 32 * ks)
+                                  : load8(x + xoff[t] + 64 * s + 32 * ks, left - 32 * ks - 8 * g);
+    };
+    auto multiply = [&](Step& d) {
+      d.q.store(0, own);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bf16x8 b = TileQ::frag(own, 16 * i, ks);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, __builtin_bit_cast(bf16x8, d.x[t][ks]), acc[t][i], 0, 0, 0);
+        }
+    };
+    int s = wave;
+    if (s < steps) load(s, s0);
+    for (; s < steps; s += 2 * W) {
+      if (s + W < steps) load(s + W, s1);
+      multiply(s0);
+      if (s + 2 * W < steps) load(s + 2 * W, s0);
+      if (s + W < steps) multiply(s1);
+    }
+    __syncthreads();  // the waves' own LDS is free
+    join_few<4, NT>(acc, reinterpret_cast<float*>(lds), drows + (int64_t)(lo + c0) * K + k0, K, used, cols);
+  }
+}
+
+// dW of one expert, or one of `parts` shares of it (the rows' steps of 64 taken in
+// equal runs; FP32, share i at out + i * E * N * K): P dout's columns, Q the rows'.
+template <int BM, int BN, int WM, int WN, int SETS, int SHARES, typename OUT>
+__global__ __launch_bounds__(64 * WM * WN * SHARES) void k_bf16_grouped_wgrad(const uint16_t* __restrict__ dout, int64_t N,
                                                                      const uint16_t* __restrict__ rows, int64_t K,
-                                                                     Groups gr, void* __restrict__ out) {
-  typedef Product<BM, BN, WM, WN, true, true> P;
+                                                                     Groups gr, int parts, OUT* __restrict__ out) {
+  typedef Product<BM, BN, WM, WN, true, true, SETS, SHARES> P;
   extern __shared__ char lds[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave / WN, wn = wave % WN;
-  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-  const int e = blockIdx.z, m0 = blockIdx.y * BM, n0 = blockIdx.x * BN;
-  int lo = 0, cnt = gr.r_cap;
-  if (gr.counts) {
-    lo = min(max(gr.offsets[e], 0), gr.r_cap);
-    cnt = min(max(gr.counts[e], 0), gr.r_cap - lo);
+  const int tm = (int)((N + BM - 1) / BM), tn = (int)((K + BN - 1) / BN);
+  // Every XCD takes a run of each share's tiles: experts differ in their rows, and a run
+  // of whole experts would leave most XCDs idle (16 experts of 1592 x 3304, loads by
+  // 1 / rank^1.2: 585 -> 199 us).
+  const int chunk = (tm * tn + 7) >> 3, at = (int)(blockIdx.x >> 3), group = at / chunk;
+  const int part = group / gr.experts, e = group - part * gr.experts;
+  const int id = (int)((blockIdx.x + group + part) & 7) * chunk + at - group * chunk;  // few tiles: not always the same XCDs
+  if (id >= tm * tn) return;
+  int i, j;
+  banded(id, tm, tn, i, j);
+  const int m0 = i * BM, n0 = j * BN;
+  int lo, hi, cnt, tiles;
+  group_rows(gr, e, BM, lo, hi, cnt, tiles);
+  if (parts > 1) {
+    const int run = ((cnt + parts - 1) / parts + kBK - 1) / kBK * kBK, first = min(part * run, cnt);
+    lo += first;
+    cnt = min(cnt - first, run);
   }
   P prod;
   prod.run(lds, dout + (int64_t)lo * N + m0, N, (int)min((int64_t)BM, N - m0), rows + (int64_t)lo * K + n0, K,
            (int)min((int64_t)BN, K - n0), cnt);
+  if (wave >= WM * WN) return;
   const int m = m0 + wm * P::MT * 16, n = n0 + wn * 64;
-  const int64_t at = ((int64_t)e * N + m) * K + n;
-  if (!F32) {
-    store_block64<P::MT>(prod.acc, lds + wave * P::MT * 2048, (uint16_t*)out + at, K, (int)(N - m), (int)(N - m),
-                         (int)min((int64_t)64, K - n));
-  } else {
-    float* o = (float*)out + at;
+  OUT* o = out + ((int64_t)group * N + m) * K + n;
+  const int rest = (int)(N - m), cols = (int)min((int64_t)64, K - n);
+  if constexpr (sizeof(OUT) == 2) store_block64<P::MT>(prod.acc, lds + wave * P::MT * 2048, o, K, rest, rest, cols);
+  else store_block64<P::MT>(prod.acc, lds + wave * P::MT * 2048, o, K, rest, cols);
+}
+
+// The shares' sums, in their order: 4 values a lane.
+template <typename OUT>
+__global__ __launch_bounds__(256) void k_wgrad_join(const float* __restrict__ part, int parts, int64_t n,
+                                                    OUT* __restrict__ out) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  const int left = (int)min(n - i, (int64_t)4);
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int p = 0; p < parts; ++p) {
+    const float* at = part + p * n + i;
+    if (left == 4) {
+      const f32x4 w = ld_any<f32x4>(at);
 #pragma unroll
-    for (int j = 0; j < P::MT; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = 16 * j + r, c = 16 * i + 4 * g;
-        if (m + row >= N) continue;
-        float* d = o + (int64_t)row * K + c;
-        if (n + c + 4 <= K) st_any<f32x4>(d, prod.acc[j][i]);
-        else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (n + c + q < K) d[q] = prod.acc[j][i][q];
-        }
-      }
+      for (int q = 0; q < 4; ++q) v[q] += w[q];
+    } else {
+      for (int q = 0; q < left; ++q) v[q] += at[q];
+    }
+  }
+  for (int q = 0; q < left; ++q) {
+    if constexpr (sizeof(OUT) == 2) out[i + q] = __builtin_bit_cast(uint16_t, (__bf16)v[q]);
+    else out[i + q] = v[q];
   }
 }
 
@@ -224,27 +504,124 @@ namespace {
 
 // Sizes of the three products: r_cap grouped rows, [width, depth] weights.
 int32_t check_sizes(int64_t r_cap, int64_t depth, int64_t width, int64_t experts, const int32_t* counts,
-                    const int32_t* offsets) {
+                    const int32_t* offsets, bool plan = true) {
   if (r_cap < 0 || depth < 1 || width < 1 || experts < 1 || experts > 1024) return EP_ERR_SHAPE;
-  if (!counts != !offsets || (!counts && experts != 1)) return EP_ERR_SHAPE;
+  if (plan && (!counts != !offsets || (!counts && experts != 1))) return EP_ERR_SHAPE;
   // a tile's rows are addressed by 32 bits of bytes, the grid by 31 bits of tiles
   if (r_cap >= ((int64_t)1 << 25) || depth > (1 << 20) || width > (1 << 20)) return EP_ERR_RANGE;
   return EP_OK;
 }
 
-template <bool QT>
-int32_t product(const uint16_t* rows, int64_t r_cap, int64_t K, const uint16_t* weight, int64_t E, int64_t N,
-                const int32_t* counts, const int32_t* offsets, uint16_t* out, hipStream_t s) {
-  if (r_cap == 0) return EP_OK;
-  if (!rows || !weight || !out) return EP_ERR_NULL;
+template <int BM, int BN, int WM, int WN, int SETS, int SHARES, bool QT>
+int32_t product_tiles(const uint16_t* rows, int64_t r_cap, int64_t K, const uint16_t* weight, int64_t E, int64_t N,
+                const int32_t* counts, const int32_t* offsets, int64_t entries, uint16_t* out, hipStream_t s) {
   const Groups gr{counts, offsets, (int)E, (int)r_cap};
-  constexpr int BM = 128, BN = 128, WM = 2, WN = 2;
-  const int64_t blocks = span_blocks(r_cap, E, !counts, BM, (N + BN - 1) / BN);
+  const int64_t blocks = span_blocks(r_cap, E, !counts, entries, BM, (N + BN - 1) / BN);
   if (blocks >= kSizeLimit) return EP_ERR_RANGE;
-  const size_t lds = Product<BM, BN, WM, WN, false, QT>::kLds;
-  hipLaunchKernelGGL((k_bf16_grouped_gemm<BM, BN, WM, WN, QT>), dim3((unsigned)blocks), dim3(64 * WM * WN), lds, s, rows, K,
+  const size_t lds = Product<BM, BN, WM, WN, false, QT, SETS, SHARES>::kLds;
+  hipLaunchKernelGGL((k_bf16_grouped_gemm<BM, BN, WM, WN, SETS, SHARES, QT>), dim3((unsigned)blocks), dim3(64 * WM * WN * SHARES), lds, s, rows, K,
                      weight, N, gr, out);
   return launch_status();
+}
+
+
+template <int RT, int NT>
+int32_t product_few(const uint16_t* rows, int64_t r_cap, int64_t K, const uint16_t* weight, int64_t E, int64_t N,
+                    const int32_t* counts, const int32_t* offsets, dim3 grid, uint16_t* out, int waves, hipStream_t s) {
+  const Groups gr{counts, offsets, (int)E, (int)r_cap};
+  const int W = K > 128 * (waves - 1) ? waves : (int)((K + 127) / 128);  // no wave without a step
+  grid.x = (unsigned)((N + 16 * RT - 1) / (16 * RT));
+  hipLaunchKernelGGL((k_bf16_grouped_few<RT, NT>), grid, dim3(64 * W), (size_t)W * RT * NT * 1024, s, rows, K, weight, N, gr,
+                     out);
+  return launch_status();
+}
+
+int32_t product_few_across(const uint16_t* dout, int64_t r_cap, int64_t N, const uint16_t* weight, int64_t E, int64_t K,
+                           const int32_t* counts, const int32_t* offsets, dim3 grid, uint16_t* drows, hipStream_t s) {
+  const Groups gr{counts, offsets, (int)E, (int)r_cap};
+  const int W = N > 64 * 7 ? 8 : (int)((N + 63) / 64);  // no wave without a step
+  grid.x = (unsigned)((K + 63) / 64);
+  hipLaunchKernelGGL(k_bf16_grouped_few_across<2>, grid, dim3(64 * W), (size_t)W * 8192, s, dout, N, weight, K, gr, drows);
+  return launch_status();
+}
+
+template <bool QT>
+int32_t product(const uint16_t* rows, int64_t r_cap, int64_t K, const uint16_t* weight, int64_t E, int64_t N,
+                const int32_t* counts, const int32_t* offsets, int64_t entries, uint16_t* out, hipStream_t s) {
+  if (r_cap == 0) return EP_OK;
+  if (!rows || !weight || !out) return EP_ERR_NULL;
+  const int64_t most = entries < r_cap ? entries : r_cap, mean = (most + E - 1) / E;
+  // Few rows an expert (on average), or so few results that tiles would leave most CUs
+  // idle: by blocks of 32 rows whose waves share out the sum.  8 experts of 4096 x 4096,
+  // 4 rows each, 47 us (tiles 77); 32 of 4096 x 7168, 8 rows 312 (384), 16 rows 318 (390),
+  // 32 rows 460 (396); 256 rows times 512 x 1024, 4 experts (512 blocks), 10.5 (13.7), times
+  // 1024 x 2048 (2048 blocks) 42 (21.5).
+  const int64_t groups = few_groups(r_cap, E, !counts), chunks = (mean + 31) / 32;
+  // Where the weights are read across, blocks are 64 columns wide, and many of them that
+  // read each weight once are better off as tiles: 8 experts of 4096 x 4096, 16 rows, 63
+  // (82); 32 of 4096 x 7168, 8 rows, 417 (386); 256 rows times 512 x 1024, 4 experts (512
+  // blocks), 16.1 (10.5).
+  const int64_t used = E < most ? E : most;  // experts with rows, at most
+  const bool few = QT ? (mean <= 24 && used * ((N + 127) / 128) <= 1024) || E * ((N + 63) / 64) * chunks <= 256
+                      : mean <= 24 || E * ((N + 31) / 32) * chunks <= 1024;
+  if (few && groups <= 65535) {
+    const dim3 grid(1, (unsigned)groups, (unsigned)(mean <= 24 ? 1 : chunks < 65535 ? chunks : 65535));
+    if constexpr (QT) return product_few_across(rows, r_cap, K, weight, E, N, counts, offsets, grid, out, s);
+    // up to 12 rows 16 at a time by eight waves: 4 rows 47 us and 64, 8 rows 320 and 312,
+    // 16 rows 430 and 318
+    else if (mean <= 12) return product_few<1, 1>(rows, r_cap, K, weight, E, N, counts, offsets, grid, out, 8, s);
+    else return product_few<2, 2>(rows, r_cap, K, weight, E, N, counts, offsets, grid, out, 4, s);
+  }
+  // Large tiles from 192 rows an expert on where they reach about half of the CUs: 8
+  // experts of 4096 x 4096, 256 rows each (128 tiles) 112 us, by small ones 162; 128 rows
+  // each 101 and 95; 4 experts of 1024 x 2048, 512 rows each (32 tiles) 48 and 33.
+  if (mean >= 192 && E * ((mean + 255) / 256) * ((N + 255) / 256) >= 112)
+    return product_tiles<256, 256, 2, 4, 1, 1, QT>(rows, r_cap, K, weight, E, N, counts, offsets, entries, out, s);
+  // Small ones: where they are fewer than the CUs two groups of waves share the sum (4
+  // experts of 1024 x 2048, 512 rows: 21.5 us, by one group 28; of 4096 x 4096, 8 rows,
+  // 95 and 77), and else two steps' loads are under way (32 of 4096 x 7168, 32 rows: 406
+  // us, with one 445; where the weights are read across 492 and 402).
+  if (E * ((mean + 127) / 128) * ((N + 127) / 128) <= 192 || (QT && mean <= 24))
+    return product_tiles<128, 128, 2, 2, 1, 2, QT>(rows, r_cap, K, weight, E, N, counts, offsets, entries, out, s);
+  return product_tiles<128, 128, 2, 2, QT ? 1 : 2, 1, QT>(rows, r_cap, K, weight, E, N, counts, offsets, entries, out, s);
+}
+
+template <int BM, int BN, int WM, int WN, int SETS, int SHARES, typename OUT>
+int32_t wgrad_tiles(const uint16_t* dout, const uint16_t* rows, int64_t width, int64_t hidden, const Groups& gr, int parts,
+                    OUT* out, hipStream_t s) {
+  const int64_t tiles = ((width + BM - 1) / BM) * ((hidden + BN - 1) / BN), blocks = parts * gr.experts * ((tiles + 7) / 8 * 8);
+  if (blocks >= kSizeLimit) return EP_ERR_RANGE;
+  const size_t lds = Product<BM, BN, WM, WN, true, true, SETS, SHARES>::kLds;
+  hipLaunchKernelGGL((k_bf16_grouped_wgrad<BM, BN, WM, WN, SETS, SHARES, OUT>), dim3((unsigned)blocks), dim3(64 * WM * WN * SHARES), lds, s, dout,
+                     width, rows, hidden, gr, parts, out);
+  return launch_status();
+}
+
+// Into how many shares an expert's rows are cut (by the mean): where 128 x 128 tiles
+// are fewer than two a CU, as many as make up for it, each of 256 rows at least.
+int wgrad_parts(int64_t width, int64_t hidden, int64_t E, int64_t entries) {
+  const int64_t tiles = E * ((width + 127) / 128) * ((hidden + 127) / 128);
+  int64_t parts = 512 / tiles, most = entries / E / 256;
+  parts = parts < most ? parts : most;
+  return (int)(parts < 2 ? 1 : parts > 16 ? 16 : parts);
+}
+
+template <typename OUT>
+int32_t wgrad(const uint16_t* dout, const uint16_t* rows, int64_t width, int64_t hidden, const Groups& gr, int64_t entries,
+              OUT* out, float* workspace, hipStream_t s) {
+  const int parts = wgrad_parts(width, hidden, gr.experts, entries);
+  if (parts > 1) {
+    const int32_t st = wgrad_tiles<128, 128, 2, 2, 2, 1>(dout, rows, width, hidden, gr, parts, workspace, s);
+    if (st != EP_OK) return st;
+    const int64_t n = gr.experts * width * hidden;
+    hipLaunchKernelGGL(k_wgrad_join<OUT>, dim3((unsigned)((n + 1023) / 1024)), dim3(256), 0, s, workspace, parts, n, out);
+    return launch_status();
+  }
+  // Large tiles where they are as many as the CUs: 8 experts of 4096 x 4096 (2048 tiles),
+  // 512 rows each, 175 us, by small ones 234; 32 of 512 x 512 (128), 4096 rows, 105 and 97.
+  if (gr.experts * ((width + 255) / 256) * ((hidden + 255) / 256) >= 256)
+    return wgrad_tiles<256, 256, 2, 4, 1, 1>(dout, rows, width, hidden, gr, 1, out, s);
+  return wgrad_tiles<128, 128, 2, 2, 2, 1>(dout, rows, width, hidden, gr, 1, out, s);
 }
 
 }  // namespace
@@ -255,7 +632,8 @@ MTB_EXPORT int32_t ep_bf16_grouped_gemm(const uint16_t* rows, int64_t r_cap, int
   const int32_t st = check_sizes(r_cap, hidden, width, num_experts, counts, offsets);
   if (st != EP_OK) return st;
   if (entries < 0) return EP_ERR_SHAPE;
-  return product<false>(rows, r_cap, hidden, weight, num_experts, width, counts, offsets, out, (hipStream_t)stream);
+  if (entries >= kSizeLimit) return EP_ERR_RANGE;
+  return product<false>(rows, r_cap, hidden, weight, num_experts, width, counts, offsets, entries, out, (hipStream_t)stream);
 }
 
 MTB_EXPORT int32_t ep_bf16_grouped_dgrad(const uint16_t* dout, int64_t r_cap, int64_t width, const uint16_t* weight,
@@ -264,12 +642,16 @@ MTB_EXPORT int32_t ep_bf16_grouped_dgrad(const uint16_t* dout, int64_t r_cap, in
   const int32_t st = check_sizes(r_cap, hidden, width, num_experts, counts, offsets);
   if (st != EP_OK) return st;
   if (entries < 0) return EP_ERR_SHAPE;
-  return product<true>(dout, r_cap, width, weight, num_experts, hidden, counts, offsets, drows, (hipStream_t)stream);
+  if (entries >= kSizeLimit) return EP_ERR_RANGE;
+  return product<true>(dout, r_cap, width, weight, num_experts, hidden, counts, offsets, entries, drows, (hipStream_t)stream);
 }
 
 MTB_EXPORT size_t ep_bf16_grouped_wgrad_workspace_bytes(int64_t width, int64_t hidden, int64_t num_experts,
                                                         int64_t entries) {
-  return 0;
+  if (check_sizes(0, hidden, width, num_experts, nullptr, nullptr, false) != EP_OK || entries < 0 || entries >= kSizeLimit)
+    return 0;
+  const int parts = wgrad_parts(width, hidden, num_experts, entries);
+  return parts > 1 ? (size_t)(parts * num_experts * width * hidden) * 4 : 0;
 }
 
 MTB_EXPORT int32_t ep_bf16_grouped_wgrad(const uint16_t* dout, const uint16_t* rows, int64_t r_cap, int64_t width,
@@ -279,16 +661,12 @@ MTB_EXPORT int32_t ep_bf16_grouped_wgrad(const uint16_t* dout, const uint16_t* r
   const int32_t st = check_sizes(r_cap, hidden, width, num_experts, counts, offsets);
   if (st != EP_OK) return st;
   if (entries < 0) return EP_ERR_SHAPE;
+  if (entries >= kSizeLimit) return EP_ERR_RANGE;
   if (!dweight || (r_cap > 0 && (!dout || !rows))) return EP_ERR_NULL;
-  constexpr int BM = 128, BN = 128, WM = 2, WN = 2;
+  const size_t need = ep_bf16_grouped_wgrad_workspace_bytes(width, hidden, num_experts, entries);
+  if (need && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 15))) return EP_ERR_WORKSPACE;
   const Groups gr{counts, offsets, (int)num_experts, (int)r_cap};
-  const dim3 grid((unsigned)((hidden + BN - 1) / BN), (unsigned)((width + BM - 1) / BM), (unsigned)num_experts);
-  const size_t lds = Product<BM, BN, WM, WN, true, true>::kLds;
   if (f32)
-    hipLaunchKernelGGL((k_bf16_grouped_wgrad<BM, BN, WM, WN, true>), grid, dim3(64 * WM * WN), lds, (hipStream_t)stream, dout,
-                       width, rows, hidden, gr, dweight);
-  else
-    hipLaunchKernelGGL((k_bf16_grouped_wgrad<BM, BN, WM, WN, false>), grid, dim3(64 * WM * WN), lds, (hipStream_t)stream,
-                       dout, width, rows, hidden, gr, dweight);
-  return launch_status();
+    return wgrad(dout, rows, width, hidden, gr, entries, (float*)dweight, (float*)workspace, (hipStream_t)stream);
+  return wgrad(dout, rows, width, hidden, gr, entries, (uint16_t*)dweight, (float*)workspace, (hipStream_t)stream);
 }

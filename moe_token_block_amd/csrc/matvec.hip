@@ -10,11 +10,9 @@
 // rate; decoding, two instructions a weight, is the larger share).
 #include "common.h"
 #include "launch.h"
+#include "quad.h"
 
 namespace mtb {
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kStep = 512;  // K values of one wave step: 16 chunks of 32 per row
 constexpr int kMaxEntries = 4096;
@@ -32,33 +30,6 @@ struct WTile {
   u32x4 c[4];
   uint2 s;  // the scale bytes of chunks 4 g .. 4 g + 3 of row 4 b + c
 };
-
-// The neighbour's value (lane ^ 1 or lane ^ 2) where `take`, else own.
-template <int CTRL>
-__device__ __forceinline__ uint32_t quad_mix(bool take, uint32_t other, uint32_t own) {
-  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)other, CTRL, 0xF, 0xF, true);
-  return take ? o : own;
-}
-
-__device__ __forceinline__ void quad_transpose(u32x4* c) {
-  const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
-#pragma unroll
-  for (int p = 0; p < 4; p += 2)
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const uint32_t x = c[p][w], y = c[p + 1][w];
-      c[p][w] = quad_mix<0xB1>(odd, y, x);
-      c[p + 1][w] = quad_mix<0xB1>(!odd, x, y);
-    }
-#pragma unroll
-  for (int p = 0; p < 2; ++p)
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const uint32_t x = c[p][w], y = c[p + 2][w];
-      c[p][w] = quad_mix<0x4E>(high, y, x);
-      c[p + 2][w] = quad_mix<0x4E>(!high, x, y);
-    }
-}
 
 __device__ __forceinline__ bf16x8 decode8(uint32_t w, float s, float t) {
   const f32x2 p0 = fp4_unpack2<0>(w, t), p1 = fp4_unpack2<1>(w, t), p2 = fp4_unpack2<2>(w, t), p3 = fp4_unpack2<3>(w, t);

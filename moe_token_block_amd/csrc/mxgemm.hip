@@ -17,6 +17,10 @@ namespace mtb {
 
 constexpr int kE2M1 = 4, kE4M3 = 0;  // the instruction's operand formats
 
+__device__ __forceinline__ i32x8 wide(u32x4 lo, u32x4 hi) {
+  return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+}
+
 // Where chunk c (16 bytes) of a tile row lies in LDS, so that eight lanes reading
 // one chunk of eight neighbouring rows meet every bank once.
 template <int RB>
@@ -48,40 +52,50 @@ struct MxTile {
       soff[i] = (uint32_t)(min(p / (SB / 4), c_n - 1) * (uint32_t)row_blocks + 4 * (p % (SB / 4)));
     }
   }
-  // bytes and blocks: what is left of a row from the step's first value on.
-  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, int bytes, int blocks) {
-    const bool whole = blocks >= SB;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int p = threadIdx.x + i * THREADS;
-      if (whole) v[i] = ld_any<u32x4>(codes + off[i]);
-      else v[i] = 16 * (p % kRowPieces) < bytes ? ld_any<u32x4>(codes + off[i]) : u32x4{0u, 0u, 0u, 0u};
-    }
+  // bytes and blocks: what is left of a row from the step's first value on; values
+  // past it are zeros.
+  template <bool EDGE>
+  __device__ __forceinline__ void load_piece(int i, const uint8_t* codes, int bytes) {
+    const int p = threadIdx.x + i * THREADS;
+    if (!EDGE || 16 * (p % kRowPieces) < bytes) v[i] = ld_any<u32x4>(codes + off[i]);
+    else v[i] = u32x4{0u, 0u, 0u, 0u};
+  }
+  template <bool EDGE>
+  __device__ __forceinline__ void load_scales(const uint8_t* scales, int blocks) {
 #pragma unroll
     for (int i = 0; i < kSc; ++i) {
-      const int p = min((int)threadIdx.x + i * THREADS, kWords - 1), n = blocks - 4 * (p % (SB / 4));
-      if (whole) {
+      if (!EDGE) {
         sv[i] = ld_any<uint32_t>(scales + soff[i]);
-      } else {
-        uint32_t w = 0;
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          if (b < n) w |= (uint32_t)scales[soff[i] + b] << (8 * b);
-        sv[i] = w;
+        continue;
       }
+      const int p = min((int)threadIdx.x + i * THREADS, kWords - 1), n = blocks - 4 * (p % (SB / 4));
+      sv[i] = 0;
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (b < n) sv[i] |= (uint32_t)scales[soff[i] + b] << (8 * b);
     }
   }
-  __device__ __forceinline__ void store(char* lds) const {
+  template <bool EDGE>
+  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, int bytes, int blocks) {
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int p = threadIdx.x + i * THREADS;
-      *reinterpret_cast<u32x4*>(lds + chunk_at<RB>(p / kRowPieces, p % kRowPieces)) = v[i];
-    }
+    for (int i = 0; i < kPieces; ++i) load_piece<EDGE>(i, codes, bytes);
+    load_scales<EDGE>(scales, blocks);
+  }
+  __device__ __forceinline__ void store_piece(int i, char* lds) const {
+    const int p = threadIdx.x + i * THREADS;
+    *reinterpret_cast<u32x4*>(lds + chunk_at<RB>(p / kRowPieces, p % kRowPieces)) = v[i];
+  }
+  __device__ __forceinline__ void store_scales(char* lds) const {
 #pragma unroll
     for (int i = 0; i < kSc; ++i) {
       const int p = threadIdx.x + i * THREADS;
       if (kWords % THREADS == 0 || p < kWords) *reinterpret_cast<uint32_t*>(lds + C * RB + 4 * p) = sv[i];
     }
+  }
+  __device__ __forceinline__ void store(char* lds) const {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) store_piece(i, lds);
+    store_scales(lds);
   }
 };
 
@@ -97,11 +111,11 @@ struct MxProduct {
   static constexpr int kOut = WM * WN * MT * 2048, kLds = 2 * kBuf > kOut ? 2 * kBuf : kOut;
   f32x4 acc[MT][NT];
 
-  static __device__ __forceinline__ i32x8 wide(u32x4 lo, u32x4 hi) {
-    return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-  }
-
-  __device__ __forceinline__ void compute(const char* a_lds, const char* w_lds, int wm, int wn) {
+  // A step's products in kParts parts, `between(part)` called before each: the lanes'
+  // scales and operands come from LDS as they are needed.
+  static constexpr int kParts = A8 ? MT : 8;
+  template <typename F>
+  __device__ __forceinline__ void compute(const char* a_lds, const char* w_lds, int wm, int wn, F&& between) {
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const u32x4 none = {0u, 0u, 0u, 0u};
     int sa[MT], sw[NT];
@@ -115,41 +129,45 @@ struct MxProduct {
       const char* at = a_lds + BM * 128 + (16 * (wm * MT + j) + r) * SB;
       sa[j] = A8 ? (int)*reinterpret_cast<const uint8_t*>(at + g) : (int)*reinterpret_cast<const uint16_t*>(at + 2 * g);
     }
-    if (A8) {
-      // lane group g: weights 32 g .. + 31, row values 16 g .. + 15 and 64 + 16 g .. + 15,
-      // the scale of values 32 g .. + 31, as the instruction has them
-      u32x4 w[NT];
+    u32x4 w[NT];
+    static_for<0, kParts>([&](auto part) {
+      constexpr int c = decltype(part)::value;
+      if constexpr (A8) {
+        // lane group g: weights 32 g .. + 31, row values 16 g .. + 15 and 64 + 16 g .. + 15,
+        // the scale of values 32 g .. + 31, as the instruction has them
+        if constexpr (c == 0) {
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-        w[i] = *reinterpret_cast<const u32x4*>(w_lds + chunk_at<kRowW>(16 * (wn * NT + i) + r, g));
-#pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        const int row = 16 * (wm * MT + j) + r;
+          for (int i = 0; i < NT; ++i)
+            w[i] = *reinterpret_cast<const u32x4*>(w_lds + chunk_at<kRowW>(16 * (wn * NT + i) + r, g));
+        }
+        between(part);
+        const int row = 16 * (wm * MT + c) + r;
         const i32x8 a = wide(*reinterpret_cast<const u32x4*>(a_lds + chunk_at<128>(row, g)),
                              *reinterpret_cast<const u32x4*>(a_lds + chunk_at<128>(row, 4 + g)));
 #pragma unroll
         for (int i = 0; i < NT; ++i)
-          acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(w[i], none), a, acc[j][i], kE2M1, kE4M3, 0,
-                                                                       sw[i], 0, sa[j]);
+          acc[c][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(w[i], none), a, acc[c][i], kE2M1, kE4M3, 0,
+                                                                       sw[i], 0, sa[c]);
+      } else {
+        // which blocks of 32 a lane group takes is free: 2 g in the first half, 2 g + 1
+        // in the second, so that one 16-bit read has both scales
+        constexpr int S = c / 4, J = MT / 4;
+        if constexpr (c % 4 == 0) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+            w[i] = *reinterpret_cast<const u32x4*>(w_lds + chunk_at<kRowW>(16 * (wn * NT + i) + r, 2 * g + S));
+        }
+        between(part);
+#pragma unroll
+        for (int j = c % 4 * J; j < (c % 4 + 1) * J; ++j) {
+          const u32x4 a = *reinterpret_cast<const u32x4*>(a_lds + chunk_at<128>(16 * (wm * MT + j) + r, 2 * g + S));
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+            acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(w[i], none), wide(a, none), acc[j][i], kE2M1,
+                                                                         kE2M1, S, sw[i], S, sa[j]);
+        }
       }
-    } else {
-      // which blocks of 32 a lane group takes is free: 2 g in the first half, 2 g + 1
-      // in the second, so that one 16-bit read has both scales
-#define MTB_HALF(S)                                                                                                  \
-  do {                                                                                                               \
-    u32x4 w[NT];                                                                                                     \
-    _Pragma("unroll") for (int i = 0; i < NT; ++i) w[i] =                                                            \
-        *reinterpret_cast<const u32x4*>(w_lds + chunk_at<kRowW>(16 * (wn * NT + i) + r, 2 * g + S));                 \
-    _Pragma("unroll") for (int j = 0; j < MT; ++j) {                                                                 \
-      const u32x4 a = *reinterpret_cast<const u32x4*>(a_lds + chunk_at<128>(16 * (wm * MT + j) + r, 2 * g + S));     \
-      _Pragma("unroll") for (int i = 0; i < NT; ++i) acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(   \
-          wide(w[i], none), wide(a, none), acc[j][i], kE2M1, kE2M1, S, sw[i], S, sa[j]);                             \
-    }                                                                                                                \
-  } while (0)
-      MTB_HALF(0);
-      MTB_HALF(1);
-#undef MTB_HALF
-    }
+    });
   }
 
   __device__ __forceinline__ void run(char* lds, const uint8_t* a, const uint8_t* as, int a_n, const uint8_t* w,
@@ -165,14 +183,22 @@ struct MxProduct {
     ta.init(A8 ? K : K / 2, K / 32, a_n);
     tw.init(K / 2, K / 32, w_n);
     int left = K;
-    auto load = [&]() {
-      ta.load(a, as, A8 ? left : left / 2, left / 32);
-      tw.load(w, ws, left / 2, left / 32);
+    auto advance = [&]() {
       a += 128;
       as += SB;
       w += kRowW;
       ws += SB;
       left -= kStep;
+    };
+    auto load = [&]() {
+      if (left >= kStep) {
+        ta.template load<false>(a, as, 0, 0);
+        tw.template load<false>(w, ws, 0, 0);
+      } else {
+        ta.template load<true>(a, as, A8 ? left : left / 2, left / 32);
+        tw.template load<true>(w, ws, left / 2, left / 32);
+      }
+      advance();
     };
     load();
     ta.store(lds);
@@ -180,15 +206,43 @@ struct MxProduct {
     if (left > 0) load();
     const int steps = (K + kStep - 1) / kStep;
     __syncthreads();
-    for (int t = 0; t < steps; ++t) {
+    // The steps whose loads (two steps ahead) are whole: the next step's values on their
+    // way to LDS and the one after's to the registers they leave, between the products.
+    int t = 0;
+    for (; t < K / kStep - 2; ++t) {
+      const char* cur = lds + ((t & 1) ? kBuf : 0);
+      char* next = lds + ((t & 1) ? 0 : kBuf);
+      compute(cur, cur + TileA::kBytes, wm, wn, [&](auto part) {
+        constexpr int c = decltype(part)::value, P = TileA::kPieces + TileW::kPieces;
+        if constexpr (c == 0) {
+          ta.store_scales(next);
+          tw.store_scales(next + TileA::kBytes);
+          ta.template load_scales<false>(as, 0);
+          tw.template load_scales<false>(ws, 0);
+        }
+        static_for<c * P / kParts, (c + 1) * P / kParts>([&](auto piece) {
+          constexpr int i = decltype(piece)::value;
+          if constexpr (i < TileA::kPieces) {
+            ta.store_piece(i, next);
+            ta.template load_piece<false>(i, a, 0);
+          } else {
+            tw.store_piece(i - TileA::kPieces, next + TileA::kBytes);
+            tw.template load_piece<false>(i - TileA::kPieces, w, 0);
+          }
+        });
+      });
+      advance();
+      __syncthreads();
+    }
+    for (; t < steps; ++t) {
+      const char* cur = lds + ((t & 1) ? kBuf : 0);
       char* next = lds + ((t & 1) ? 0 : kBuf);
       if (t + 1 < steps) {
         ta.store(next);
         tw.store(next + TileA::kBytes);
         if (left > 0) load();
       }
-      const char* buf = lds + ((t & 1) ? kBuf : 0);
-      compute(buf, buf + TileA::kBytes, wm, wn);
+      compute(cur, cur + TileA::kBytes, wm, wn, [](auto) {});
       __syncthreads();
     }
   }
@@ -205,7 +259,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mxfp4_grouped_gemm(const uint8
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave / WN, wn = wave % WN;
   Span s;
   int tn;
-  if (!find_span<BM>(gr, (int)((N + BN - 1) / BN), s, tn, 8)) return;
+  if (!find_span<BM>(gr, (int)((N + BN - 1) / BN), s, tn)) return;
   P prod;
   const int n0 = tn * BN;
   const int64_t row = s.row0, col = (int64_t)s.expert * N + n0;
@@ -216,8 +270,131 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mxfp4_grouped_gemm(const uint8
     prod.run(lds, data, scales, 1, wcodes, wscales, 1, 0);
   static_assert(P::NT == 4, "a wave stores 64 columns");
   const int m = wm * P::MT * 16, n = n0 + wn * 64;
+  if (s.extent > BM)
+    clear_rows(out + (int64_t)s.row0 * N + n0, N, BM, s.extent, (int)min((int64_t)BN, N - n0));
   store_block64<P::MT>(prod.acc, lds + wave * P::MT * 2048, out + (row + m) * N + n, N, s.used - m, s.extent - m,
                        (int)min((int64_t)64, N - n));
+}
+
+// For experts with few rows, where the time is that of reading the weights.  A
+// workgroup takes 16 RT weight rows of one expert and 16 NT of its rows at a time (the
+// z-th of gridDim.z first, then every gridDim.z-th); its waves take the sum's steps of
+// 512 values in turn and join their sums through LDS.  Codes go from memory to
+// registers, four lanes on 64 contiguous bytes, and are brought into the instruction's
+// order within lane quads; a step's loads are in flight while the step before is
+// multiplied.
+template <int RT, int NT, bool A8>
+__global__ __launch_bounds__(NT == 1 ? 512 : 256) void k_mxfp4_grouped_few(
+    const uint8_t* __restrict__ data, const uint8_t* __restrict__ scales, int K, const uint8_t* __restrict__ wcodes,
+    const uint8_t* __restrict__ wscales, int64_t N, Groups gr, uint16_t* __restrict__ out) {
+  extern __shared__ char lds[];
+  float* red = reinterpret_cast<float*>(lds);  // [waves][RT * NT][16 rows][16 columns]
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), W = blockDim.x >> 6;
+  const int n0 = (int)blockIdx.x * 16 * RT, cols = (int)min((int64_t)16 * RT, N - n0), e = blockIdx.y;
+  int lo, hi, cnt;
+  if (!few_rows(gr, lo, hi, cnt)) return;
+  if (blockIdx.z == 0) clear_rows(out + (int64_t)lo * N + n0, N, cnt, hi - lo, cols);
+
+  // lane 16 g + 4 b + c loads, for j = 0..3, chunk 4 g + c (32 values) of row 4 b + j; the
+  // quad's exchange leaves chunk 4 g + j of row 4 b + c in register j, lane group g's block
+  // of the j-th product.  Of MXFP8 rows the instruction wants, beside a group's block
+  // scales, 16 values of block g / 2 and 16 of block 2 + g / 2: chunks of 16 values.
+  const int g = lane >> 4, r = lane & 15, b4 = lane & 12, c = lane & 3;
+  const int wchunk = 4 * g + c, xchunk = A8 ? 8 * (g >> 1) + 2 * c + (g & 1) : wchunk;
+  const uint32_t wrow = K / 2, xrow = A8 ? K : K / 2, srow = K / 32;
+  const int64_t col = (int64_t)e * N + n0;
+  const uint8_t* w = wcodes + col * wrow + 16 * wchunk;
+  const uint8_t* ws = wscales + col * srow + 4 * g;
+  uint32_t woff[RT][4], wsoff[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) woff[i][j] = (uint32_t)min(16 * i + b4 + j, cols - 1) * wrow;
+    wsoff[i] = (uint32_t)min(16 * i + r, cols - 1) * srow;
+  }
+  const int steps = (K + 511) / 512;
+  constexpr int H = A8 ? 2 : 1;
+  struct Step {
+    u32x4 w[RT][4], x[NT][H][4];
+    uint32_t sw[RT], sx[NT];
+  };
+  auto scale4 = [](const uint8_t* p, int n) {
+    if (n >= 4) return ld_any<uint32_t>(p);
+    uint32_t v = 0;
+#pragma unroll
+    for (int b = 0; b < 3; ++b)
+      if (b < n) v |= (uint32_t)p[b] << (8 * b);
+    return v;
+  };
+  for (int c0 = 16 * NT * (int)blockIdx.z; c0 < cnt; c0 += 16 * NT * (int)gridDim.z) {
+    const int used = min(cnt - c0, 16 * NT);
+    const uint8_t* x = data + (int64_t)(lo + c0) * xrow + 16 * xchunk;
+    const uint8_t* xs = scales + (int64_t)(lo + c0) * srow + 4 * g;
+    uint32_t xoff[NT][4], xsoff[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) xoff[i][j] = (uint32_t)min(16 * i + b4 + j, used - 1) * xrow;
+      xsoff[i] = (uint32_t)min(16 * i + r, used - 1) * srow;
+    }
+    f32x4 acc[NT][RT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < RT; ++i) acc[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto load = [&](int s, Step& d) {
+      const u32x4 none = {0u, 0u, 0u, 0u};
+      const int left = K - 512 * s;  // values from the step's first on
+      const bool whole = left >= 512;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+          d.w[i][j] = whole || 32 * wchunk < left ? ld_any<u32x4>(w + woff[i][j] + 256 * s) : none;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+            d.x[i][h][j] = whole || (A8 ? 16 * (xchunk + 16 * h) : 32 * xchunk) < left
+                               ? ld_any<u32x4>(x + xoff[i][j] + (A8 ? 512 : 256) * s + 256 * h)
+                               : none;
+      }
+      const int blocks = whole ? 4 : left / 32 - 4 * g;
+#pragma unroll
+      for (int i = 0; i < RT; ++i) d.sw[i] = scale4(ws + wsoff[i] + 16 * s, blocks);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) d.sx[i] = scale4(xs + xsoff[i] + 16 * s, blocks);
+    };
+    auto multiply = [&](Step& d) {
+      const u32x4 none = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int i = 0; i < RT; ++i) quad_transpose(d.w[i]);
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int h = 0; h < H; ++h) quad_transpose(d.x[i][h]);
+      static_for<0, 4>([&](auto block) {
+        constexpr int j = decltype(block)::value;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < RT; ++i)
+            acc[t][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                wide(d.w[i][j], none), wide(d.x[t][0][j], A8 ? d.x[t][H - 1][j] : none), acc[t][i], kE2M1,
+                A8 ? kE4M3 : kE2M1, j, (int)d.sw[i], j, (int)d.sx[t]);
+      });
+    };
+    Step s0, s1;
+    int s = wave;
+    if (s < steps) load(s, s0);
+    for (; s < steps; s += 2 * W) {
+      if (s + W < steps) load(s + W, s1);
+      multiply(s0);
+      if (s + 2 * W < steps) load(s + 2 * W, s0);
+      if (s + W < steps) multiply(s1);
+    }
+    join_few<RT, NT>(acc, red, out + (int64_t)(lo + c0) * N + n0, N, used, cols);
+  }
 }
 
 }  // namespace mtb
@@ -225,18 +402,55 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mxfp4_grouped_gemm(const uint8
 using namespace mtb;
 
 namespace {
-template <bool A8>
-int32_t mx_product(const uint8_t* data, const uint8_t* scales, int64_t r_cap, int64_t K, const uint8_t* wcodes,
+template <int BM, int BN, int WM, int WN, bool A8>
+int32_t mx_tiles(const uint8_t* data, const uint8_t* scales, int64_t r_cap, int64_t K, const uint8_t* wcodes,
                    const uint8_t* wscales, int64_t E, int64_t N, const int32_t* counts, const int32_t* offsets,
-                   uint16_t* out, hipStream_t s) {
-  constexpr int BM = 128, BN = 128, WM = 2, WN = 2;
+                   int64_t entries, uint16_t* out, hipStream_t s) {
   const Groups gr{counts, offsets, (int)E, (int)r_cap};
-  const int64_t blocks = span_blocks(r_cap, E, !counts, BM, (N + BN - 1) / BN);
+  const int64_t blocks = span_blocks(r_cap, E, !counts, entries, BM, (N + BN - 1) / BN);
   if (blocks >= kSizeLimit) return EP_ERR_RANGE;
   const size_t lds = MxProduct<BM, BN, WM, WN, A8>::kLds;
   hipLaunchKernelGGL((k_mxfp4_grouped_gemm<BM, BN, WM, WN, A8>), dim3((unsigned)blocks), dim3(64 * WM * WN), lds, s, data,
                      scales, (int)K, wcodes, wscales, N, gr, out);
   return launch_status();
+}
+
+template <int RT, int NT, bool A8>
+int32_t mx_few(const uint8_t* data, const uint8_t* scales, int64_t r_cap, int64_t K, const uint8_t* wcodes,
+               const uint8_t* wscales, int64_t E, int64_t N, const int32_t* counts, const int32_t* offsets, dim3 grid,
+               uint16_t* out, int waves, hipStream_t s) {
+  const Groups gr{counts, offsets, (int)E, (int)r_cap};
+  const int W = K > 512 * (waves - 1) ? waves : (int)((K + 511) / 512);  // no wave without a step
+  grid.x = (unsigned)((N + 16 * RT - 1) / (16 * RT));
+  hipLaunchKernelGGL((k_mxfp4_grouped_few<RT, NT, A8>), grid, dim3(64 * W), (size_t)W * RT * NT * 1024, s, data, scales,
+                     (int)K, wcodes, wscales, N, gr, out);
+  return launch_status();
+}
+
+template <bool A8>
+int32_t mx_product(const uint8_t* data, const uint8_t* scales, int64_t r_cap, int64_t K, const uint8_t* wcodes,
+                   const uint8_t* wscales, int64_t E, int64_t N, const int32_t* counts, const int32_t* offsets,
+                   int64_t entries, uint16_t* out, hipStream_t s) {
+  const int64_t most = entries < r_cap ? entries : r_cap, mean = (most + E - 1) / E;
+  const int64_t groups = few_groups(r_cap, E, !counts);
+  // Up to 16 rows an expert (on average) by the kernel that streams the weights, MXFP4
+  // rows 32 weight rows at a time, MXFP8 rows, which take twice the registers, 16: 32
+  // experts of 4096 x 7168, 8 rows each, 99 us (tiles 137) and 141 (192); 16 rows 132
+  // (140) and 193 (197); 32 rows 199 (148) and 297 (207).
+  // With more rows, too, where a long sum would be left to few tiles: a workgroup for
+  // each 16 rows.
+  constexpr int RT = A8 ? 1 : 2;
+  const int64_t chunks = (mean + 15) / 16;
+  const bool thin = K > 2048 && E * ((N + 16 * RT - 1) / (16 * RT)) * chunks <= 2048 && chunks <= 65535;
+  if ((mean <= 16 || thin) && groups <= 65535)
+    return mx_few<RT, 1, A8>(data, scales, r_cap, K, wcodes, wscales, E, N, counts, offsets,
+                             dim3(1, (unsigned)groups, (unsigned)chunks), out, 4, s);
+  // Large tiles from 192 rows an expert on where they reach about half of the CUs: 8
+  // experts of 4096 x 4096, 259 rows each (256 tiles), 40 us, by small ones 52; 128 rows
+  // each 35 and 31; 4 experts of 1024 x 2048, 512 rows each (32 tiles), 22 and 13.
+  if (mean >= 192 && E * ((mean + 255) / 256) * ((N + 255) / 256) >= 112)
+    return mx_tiles<256, 256, 2, 4, A8>(data, scales, r_cap, K, wcodes, wscales, E, N, counts, offsets, entries, out, s);
+  return mx_tiles<128, 128, 2, 2, A8>(data, scales, r_cap, K, wcodes, wscales, E, N, counts, offsets, entries, out, s);
 }
 }  // namespace
 
@@ -248,12 +462,12 @@ MTB_EXPORT int32_t ep_mxfp4_grouped_gemm(const uint8_t* data, const uint8_t* sca
     return EP_ERR_SHAPE;
   if (entries < 0 || !counts != !offsets || (!counts && num_experts != 1)) return EP_ERR_SHAPE;
   if (row_format != EP_ROWS_MXFP4 && row_format != EP_ROWS_MXFP8) return EP_ERR_DTYPE;
-  if (r_cap >= ((int64_t)1 << 25) || hidden > (1 << 20) || width > (1 << 20)) return EP_ERR_RANGE;
+  if (entries >= kSizeLimit || r_cap >= ((int64_t)1 << 25) || hidden > (1 << 20) || width > (1 << 20)) return EP_ERR_RANGE;
   if (r_cap == 0) return EP_OK;
   if (!data || !scales || !weight_codes || !weight_scales || !out) return EP_ERR_NULL;
   if (row_format == EP_ROWS_MXFP8)
     return mx_product<true>(data, scales, r_cap, hidden, weight_codes, weight_scales, num_experts, width, counts, offsets,
-                            out, (hipStream_t)stream);
+                            entries, out, (hipStream_t)stream);
   return mx_product<false>(data, scales, r_cap, hidden, weight_codes, weight_scales, num_experts, width, counts, offsets,
-                           out, (hipStream_t)stream);
+                           entries, out, (hipStream_t)stream);
 }

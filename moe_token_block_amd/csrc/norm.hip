@@ -14,8 +14,8 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // A row is a workgroup's: thread i has its chunks of 8 values i, i + THREADS, ...
 // (NB of them), kept in registers between the sum and its use.
-template <int THREADS>
-__device__ __forceinline__ float block_sum(float v, float* red) {
+template <int THREADS, typename T>
+__device__ __forceinline__ T block_sum(T v, T* red) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
   if (THREADS == 64) return v;
@@ -61,7 +61,7 @@ __global__ __launch_bounds__(THREADS) void k_rmsnorm_mxfp8(const uint16_t* x, co
                                                            const uint16_t* __restrict__ weight, int H, float eps,
                                                            uint16_t* h_out, uint8_t* __restrict__ data,
                                                            uint8_t* __restrict__ scales, float* __restrict__ rstd) {
-  __shared__ float red[THREADS / 64];
+  __shared__ double red[THREADS / 64];
   const int tid = threadIdx.x, nch = H >> 3;
   const int64_t row = blockIdx.x, c0 = row * nch;
   u32x4 v[NB], q[NB];
@@ -74,7 +74,7 @@ __global__ __launch_bounds__(THREADS) void k_rmsnorm_mxfp8(const uint16_t* x, co
       if (RES) q[b] = ld_once<u32x4>(res + 8 * (c0 + c));
     }
   }
-  float ss = 0.0f;
+  double ss = 0.0;
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     const int c = tid + b * THREADS;
@@ -84,13 +84,17 @@ __global__ __launch_bounds__(THREADS) void k_rmsnorm_mxfp8(const uint16_t* x, co
         v[b][i] = bf16pair(bf16lo(v[b][i]) + bf16lo(q[b][i]), bf16hi(v[b][i]) + bf16hi(q[b][i]));
       if (c < nch) st_once(h_out + 8 * (c0 + c), v[b]);
     }
-    float f[8];
+    float f[8], part = 0.0f;
     unpack8(v[b], f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(f[i], f[i], ss);
+    for (int i = 0; i < 8; ++i) part = __builtin_fmaf(f[i], f[i], part);
+    ss += part;
   }
+  // eight squares at a time in FP32, their sums in FP64: rstd is the nearest FP32 number
+  // but for a few in a thousand rows, and with it nearly every byte what exact
+  // arithmetic gives
   ss = block_sum<THREADS>(ss, red);
-  const float r = 1.0f / sqrtf(ss / (float)H + eps);
+  const float r = (float)(1.0 / sqrt(ss / H + (double)eps));
   if (tid == 0) rstd[row] = r;
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
@@ -196,9 +200,9 @@ __global__ __launch_bounds__(THREADS) void k_drmsnorm(const uint16_t* __restrict
   for (int b = 0; b < NB; ++b) {
     const int c = tid + b * THREADS;
     if (c >= nch) continue;
-    f32x4* o = reinterpret_cast<f32x4*>(part + ((int64_t)blockIdx.x * nch + c) * 8);
-    o[0] = f32x4{dw[b][0], dw[b][1], dw[b][2], dw[b][3]};
-    o[1] = f32x4{dw[b][4], dw[b][5], dw[b][6], dw[b][7]};
+    float* o = part + ((int64_t)blockIdx.x * nch + c) * 8;
+    st_any<f32x4>(o, f32x4{dw[b][0], dw[b][1], dw[b][2], dw[b][3]});
+    st_any<f32x4>(o + 4, f32x4{dw[b][4], dw[b][5], dw[b][6], dw[b][7]});
   }
 }
 
@@ -242,8 +246,12 @@ void by_width(int64_t hidden, F&& f) {
   else f(std::integral_constant<int, 512>{}, std::integral_constant<int, 4>{});
 }
 
+// Up to so many rows one workgroup takes them all and its sums are dw: one launch.
+constexpr int64_t kOneBlockRows = 4;
+
 // Workgroups of the gradient, and rows of its workspace.
 int64_t grad_parts(int64_t rows, int64_t hidden) {
+  if (rows <= kOneBlockRows) return rows > 0;
   const int64_t most = hidden <= 1024 ? 2048 : 512;
   return rows < most ? rows : most;
 }
@@ -272,7 +280,7 @@ MTB_EXPORT int32_t rmsnorm_mxfp8(const uint16_t* x, const uint16_t* residual, co
 }
 
 MTB_EXPORT size_t drmsnorm_workspace_bytes(int64_t rows, int64_t hidden) {
-  if (check_sizes(rows, hidden) != EP_OK) return 0;
+  if (check_sizes(rows, hidden) != EP_OK || rows <= kOneBlockRows) return 0;
   return (size_t)(grad_parts(rows, hidden) * hidden) * 4;
 }
 
@@ -282,19 +290,21 @@ MTB_EXPORT int32_t drmsnorm(const uint16_t* dy, const uint16_t* h, const uint16_
   const int32_t st = check_sizes(rows, hidden);
   if (st != EP_OK) return st;
   if (!dweight || (rows > 0 && (!dy || !h || !weight || !rstd || !dx))) return EP_ERR_NULL;
-  if (rows > 0 && (!workspace || workspace_bytes < drmsnorm_workspace_bytes(rows, hidden) || ((uintptr_t)workspace & 15)))
-    return EP_ERR_WORKSPACE;
+  const size_t need = drmsnorm_workspace_bytes(rows, hidden);
+  if (need && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 15))) return EP_ERR_WORKSPACE;
+  float* part = need ? (float*)workspace : dweight;
   const int parts = (int)grad_parts(rows, hidden);
   if (rows > 0)
     by_width(hidden, [&](auto threads, auto nb) {
       constexpr int TH = decltype(threads)::value, NB = decltype(nb)::value;
       if (dh)
         hipLaunchKernelGGL((k_drmsnorm<TH, NB, true>), dim3((unsigned)parts), dim3(TH), 0, (hipStream_t)stream, dy, h, weight,
-                           rstd, dh, (int)rows, (int)hidden, dx, (float*)workspace);
+                           rstd, dh, (int)rows, (int)hidden, dx, part);
       else
         hipLaunchKernelGGL((k_drmsnorm<TH, NB, false>), dim3((unsigned)parts), dim3(TH), 0, (hipStream_t)stream, dy, h, weight,
-                           rstd, dh, (int)rows, (int)hidden, dx, (float*)workspace);
+                           rstd, dh, (int)rows, (int)hidden, dx, part);
     });
+  if (parts == 1) return launch_status();
   hipLaunchKernelGGL(k_drmsnorm_weight, dim3((unsigned)((hidden + 63) / 64)), dim3(1024), 0, (hipStream_t)stream,
                      (const float*)workspace, parts, (int)hidden, dweight);
   return launch_status();

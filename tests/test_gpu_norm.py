@@ -174,7 +174,7 @@ def test_refusals(dev):
                  lambda: mtb.rmsnorm_mxfp8(bf(4, 64), bf(64), h=bf(4, 64)),
                  lambda: mtb.drmsnorm(bf(4, 64), bf(4, 64), bf(64), f32.double()),
                  lambda: mtb.drmsnorm(bf(4, 64), bf(3, 64), bf(64), f32),
-                 lambda: mtb.drmsnorm(bf(4, 64), bf(4, 64), bf(64), f32, workspace=torch.zeros(8, dtype=torch.uint8, device=dev))):
+                 lambda: mtb.drmsnorm(bf(40, 64), bf(40, 64), bf(64), torch.zeros(40, device=dev), workspace=torch.zeros(8, dtype=torch.uint8, device=dev))):
         with pytest.raises((ValueError, TypeError)):
             call()
     for call in (lambda: mtb.rmsnorm_mxfp8(bf(1, 16416), bf(16416)), lambda: mtb.rmsnorm_mxfp8(bf(1, 64), bf(64), eps=-1.0),

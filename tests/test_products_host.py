@@ -85,14 +85,14 @@ def test_validation_before_launch(lib):
     assert n(N, N, P, 4, 64, 1e-6, N, P, P, P, N) == -1
     assert n(N, N, N, 0, 64, 1e-6, N, N, N, N, N) == 0
     d = lib.drmsnorm
-    ws = lib.drmsnorm_workspace_bytes(4, 64)
-    assert ws > 0 and lib.drmsnorm_workspace_bytes(0, 64) == 0 and lib.drmsnorm_workspace_bytes(4, 33) == 0
+    ws = lib.drmsnorm_workspace_bytes(40, 64)
+    assert ws > 0 and lib.drmsnorm_workspace_bytes(4, 64) == 0 and lib.drmsnorm_workspace_bytes(0, 64) == 0 and lib.drmsnorm_workspace_bytes(4, 33) == 0
     assert d(P, P, P, P, N, 4, 48, P, P, P, ws, N) == -2
     assert d(P, P, P, N, N, 4, 64, P, P, P, ws, N) == -1
     assert d(P, P, P, P, N, 4, 64, P, N, P, ws, N) == -1
-    assert d(P, P, P, P, N, 4, 64, P, P, P, ws - 1, N) == -7
-    assert d(P, P, P, P, N, 4, 64, P, P, N, ws, N) == -7
-    assert d(P, P, P, P, N, 4, 64, P, P, ctypes.c_void_p(0x1004), ws, N) == -7
+    assert d(P, P, P, P, N, 40, 64, P, P, P, ws - 1, N) == -7
+    assert d(P, P, P, P, N, 40, 64, P, P, N, ws, N) == -7
+    assert d(P, P, P, P, N, 40, 64, P, P, ctypes.c_void_p(0x1004), ws, N) == -7
 
 
 def test_binding_refuses_cpu_tensors(lib):
