@@ -73,27 +73,23 @@ __device__ __forceinline__ bool tile_of(uint32_t block, int tiles_m, int tiles_n
 template <int BM>
 __device__ __forceinline__ bool find_span(const Groups& gr, int tiles_n, Span& s, int& tile_n) {
   const int lane = threadIdx.x & 63;
-  int total = 0;
-  for (int base = 0; base <= gr.experts; base += 64) {
-    int lo, hi, cnt, tiles;
+  int lo, hi, cnt, tiles, upto, total = 0;
+  auto take = [&](int base) {  // 64 groups from base on, and the running sum of their tiles
     group_rows(gr, base + lane, BM, lo, hi, cnt, tiles);
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) tiles += __shfl_xor(tiles, o, 64);
-    total += tiles;
-  }
-  total = __builtin_amdgcn_readfirstlane(total);
-  int t;
-  if (!tile_of(blockIdx.x, total, tiles_n, t, tile_n)) return false;
-  // which expert the t-th belongs to
-  for (int base = 0; base <= gr.experts; base += 64) {
-    int lo, hi, cnt, tiles;
-    group_rows(gr, base + lane, BM, lo, hi, cnt, tiles);
-    int upto = tiles;
+    upto = tiles;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
       const int v = __shfl_up(upto, o, 64);
       if (lane >= o) upto += v;
     }
+    return __builtin_amdgcn_readlane(upto, 63);
+  };
+  for (int base = 0; base <= gr.experts; base += 64) total += take(base);
+  int t;
+  if (!tile_of(blockIdx.x, total, tiles_n, t, tile_n)) return false;
+  // which group the t-th belongs to
+  for (int base = 0; base <= gr.experts; base += 64) {
+    const int sum = gr.experts < 64 ? total : take(base);  // one stretch of 64: it is there already
     const uint64_t past = __builtin_amdgcn_ballot_w64(upto > t);
     if (past) {
       const int who = __builtin_ctzll(past), n = __builtin_amdgcn_readlane(tiles, who);
@@ -106,7 +102,7 @@ __device__ __forceinline__ bool find_span(const Groups& gr, int tiles_n, Span& s
       s.extent = base + who == gr.experts ? min(rest, kTailRows) : i == n - 1 ? rest : BM;
       return true;
     }
-    t -= __builtin_amdgcn_readlane(upto, 63);
+    t -= sum;
   }
   return false;
 }
@@ -126,6 +122,26 @@ __device__ __forceinline__ u32x4 load8(const uint16_t* p, int n) {
   for (int i = 0; i < 8; ++i)
     if (i < n) w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
   return u32x4{w[0], w[1], w[2], w[3]};
+}
+
+// The same where p + n is the end of a row (n may be negative): without a branch, from
+// the row's last eight values shifted down.  wide: the row has eight.
+__device__ __forceinline__ u32x4 load_end(const uint16_t* p, int n, bool wide) {
+  // kept apart from a whole load on another path: merged with it, that one would be
+  // shifted too, and waited for at once (256 rows of 1024 times 512 x 1024: 10.2 -> 15.2 us)
+  asm volatile("" : "+v"(n));
+  if (!wide) return load8(p, n);
+  const u32x4 v = ld_any<u32x4>(p - (8 - min(n, 8)));
+  const int past = 8 - max(min(n, 8), 0);  // values of p's eight that do not exist
+  const uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+  const int s = 16 * (past & 3);
+  uint64_t a = lo >> s | (s ? hi << (64 - s) : 0), b = hi >> s;
+  if (past >= 4) {
+    a = b;
+    b = 0;
+  }
+  if (past >= 8) a = 0;
+  return u32x4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
 }
 
 __device__ __forceinline__ void store8(uint16_t* p, u32x4 v, int n) {
@@ -190,6 +206,28 @@ __device__ __forceinline__ void store_block64(const f32x4 (&acc)[MT][4], char* l
       }
     }
   }
+}
+
+// The sums of two groups of waves that shared a tile's terms: the second's (share 1)
+// through LDS to the first's.  tid: within the group.
+template <int MT, int NT>
+__device__ __forceinline__ void join_shares(f32x4 (&acc)[MT][NT], char* lds, int tid, int share) {
+  f32x4* at = reinterpret_cast<f32x4*>(lds) + tid * MT * NT;
+  const int turn = tid & 7;  // a lane's pieces in another order for each of eight: no bank is met twice
+  if (share) {
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) at[(j * NT + i) ^ turn] = acc[j][i];
+  }
+  __syncthreads();
+  if (!share) {
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[j][i] += at[(j * NT + i) ^ turn];
+  }
+  __syncthreads();
 }
 
 // Rows [first, rows) and columns [0, cols) of a tile: zeros.

@@ -22,14 +22,15 @@ constexpr int kBK = 64;  // terms of the sum in one step
 template <int C, int THREADS, bool T, int SETS>
 struct Tile {
   static constexpr int kPieces = C * 8 / THREADS;  // 16-byte pieces a thread
-  int tid;                                         // of the THREADS that share the tile
+  int tid, ld;                                     // of the THREADS that share the tile; values from row to row
   uint32_t off[kPieces];                           // bytes from the step's base
   u32x4 v[SETS][kPieces];                          // of the steps whose loads are under way
 
-  // ld: values from one row of the matrix to the next; c_n: rows (R) or columns (T)
+  // row: values from one row of the matrix to the next; c_n: rows (R) or columns (T)
   // that exist from the tile's first on, at least 1.
-  __device__ __forceinline__ void init(int thread, int64_t ld, int c_n) {
+  __device__ __forceinline__ void init(int thread, int64_t row, int c_n) {
     tid = thread;
+    ld = (int)row;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int p = tid + i * THREADS;
@@ -40,14 +41,20 @@ struct Tile {
   // base: the step's first value; terms: how many of the step's 64 exist.  Rows (R) that
   // do not exist repeat the last, and pieces of columns (T) the last piece: what comes of
   // them is not stored.  EDGE: terms that do not exist are zeros, and nothing past a
-  // row's last column is read (without it up to 7 values of the next row are).
+  // row's end is read (without it up to 7 values of the next row are).
   template <bool EDGE>
   __device__ __forceinline__ void load_piece(int set, int i, const uint16_t* base, int terms, int c_n) {
     const uint16_t* src = reinterpret_cast<const uint16_t*>(reinterpret_cast<const char*>(base) + off[i]);
     const int p = tid + i * THREADS;
-    if (!EDGE) v[set][i] = ld_any<u32x4>(src);
-    else if (T) v[set][i] = load8(src, p / (C / 8) < terms ? c_n - 8 * (p % (C / 8)) : 0);
-    else v[set][i] = load8(src, terms - 8 * (p & 7));
+    if (!EDGE) {
+      v[set][i] = ld_any<u32x4>(src);
+    } else if (T) {
+      const int k = p / (C / 8), past = max(k - (terms - 1), 0);
+      v[set][i] = load_end(src - (int64_t)past * ld, c_n - 8 * min(p % (C / 8), (c_n - 1) >> 3), ld >= 8);
+      if (past) v[set][i] = u32x4{0u, 0u, 0u, 0u};
+    } else {
+      v[set][i] = load_end(src, terms - 8 * (p & 7), ld >= 8);
+    }
   }
   template <bool EDGE>
   __device__ __forceinline__ void load(int set, const uint16_t* base, int terms, int c_n) {
@@ -220,22 +227,7 @@ struct Product {
     }
     if constexpr (SHARES == 2) {  // the buffers are free: the second group's sums to the first
       static_assert(kLds >= BM * BN * 4, "the sums fit the buffers");
-      f32x4* at = reinterpret_cast<f32x4*>(all_lds) + tid * MT * NT;
-      const int turn = tid & 7;  // a lane's pieces in another order for each of eight: no bank is met twice
-      if (share) {
-#pragma unroll
-        for (int j = 0; j < MT; ++j)
-#pragma unroll
-          for (int i = 0; i < NT; ++i) at[(j * NT + i) ^ turn] = acc[j][i];
-      }
-      __syncthreads();
-      if (!share) {
-#pragma unroll
-        for (int j = 0; j < MT; ++j)
-#pragma unroll
-          for (int i = 0; i < NT; ++i) acc[j][i] += at[(j * NT + i) ^ turn];
-      }
-      __syncthreads();
+      join_shares(acc, all_lds, tid, share);
     }
   }
 };
@@ -328,9 +320,9 @@ __global__ __launch_bounds__(NT == 1 ? 512 : 256) void k_bf16_grouped_few(const 
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
 #pragma unroll
-          for (int i = 0; i < RT; ++i) d.w[i][j] = load8(w + woff[i][j] + at, left);
+          for (int i = 0; i < RT; ++i) d.w[i][j] = load_end(w + woff[i][j] + at, left, K >= 8);
 #pragma unroll
-          for (int i = 0; i < NT; ++i) d.x[i][j] = load8(x + xoff[i][j] + at, left);
+          for (int i = 0; i < NT; ++i) d.x[i][j] = load_end(x + xoff[i][j] + at, left, K >= 8);
         }
       }
     };
@@ -407,7 +399,7 @@ __global__ __launch_bounds__(512) void k_bf16_grouped_few_across(const uint16_t*
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
           d.x[t][ks] = left == 64 ? ld_any<u32x4>(x + xoff[t] + 64 * s + 32 * ks)
-                                  : load8(x + xoff[t] + 64 * s + 32 * ks, left - 32 * ks - 8 * g);
+                                  : load_end(x + xoff[t] + 64 * s + 32 * ks, left - 32 * ks - 8 * g, N >= 8);
     };
     auto multiply = [&](Step& d) {
       d.q.store(0, own);
@@ -565,11 +557,18 @@ int32_t product(const uint16_t* rows, int64_t r_cap, int64_t K, const uint16_t* 
   const bool few = QT ? (mean <= 24 && used * ((N + 127) / 128) <= 1024) || E * ((N + 63) / 64) * chunks <= 256
                       : mean <= 24 || E * ((N + 31) / 32) * chunks <= 1024;
   if (few && groups <= 65535) {
-    const dim3 grid(1, (unsigned)groups, (unsigned)(mean <= 24 ? 1 : chunks < 65535 ? chunks : 65535));
+    // workgroups beside each other for one expert's rows: as many as the mean asks for,
+    // more (the loads may be uneven) where that leaves few
+    const int64_t spare = 1024 / (E * ((N + 63) / 64)), all = (most + 31) / 32, z = chunks > spare ? chunks : spare < all ? spare : all;
+    const dim3 grid(1, (unsigned)groups, (unsigned)(z < 1 ? 1 : z < 32767 ? z : 32767));
     if constexpr (QT) return product_few_across(rows, r_cap, K, weight, E, N, counts, offsets, grid, out, s);
     // up to 12 rows 16 at a time by eight waves: 4 rows 47 us and 64, 8 rows 320 and 312,
     // 16 rows 430 and 318
-    else if (mean <= 12) return product_few<1, 1>(rows, r_cap, K, weight, E, N, counts, offsets, grid, out, 8, s);
+    // (or where that leaves few workgroups: 48 rows times 86 x 4737, 2 experts, 11.1 us and
+    // 18.1; 156 times 27 x 5888, 8 experts, 12.6 and 15.7)
+    else if (mean <= 12 || E * ((N + 15) / 16) * ((mean + 15) / 16) <= 512)
+      return product_few<1, 1>(rows, r_cap, K, weight, E, N, counts, offsets, dim3(1, grid.y, mean <= 12 ? grid.z : 2 * grid.z),
+                               out, 8, s);
     else return product_few<2, 2>(rows, r_cap, K, weight, E, N, counts, offsets, grid, out, 4, s);
   }
   // Large tiles from 192 rows an expert on where they reach about half of the CUs: 8
@@ -577,11 +576,13 @@ int32_t product(const uint16_t* rows, int64_t r_cap, int64_t K, const uint16_t* 
   // each 101 and 95; 4 experts of 1024 x 2048, 512 rows each (32 tiles) 48 and 33.
   if (mean >= 192 && E * ((mean + 255) / 256) * ((N + 255) / 256) >= 112)
     return product_tiles<256, 256, 2, 4, 1, 1, QT>(rows, r_cap, K, weight, E, N, counts, offsets, entries, out, s);
-  // Small ones: where they are fewer than the CUs two groups of waves share the sum (4
+  // Small ones: where they are fewer than the CUs (or as many, and the sum long) two
+  // groups of waves share the sum (4
   // experts of 1024 x 2048, 512 rows: 21.5 us, by one group 28; of 4096 x 4096, 8 rows,
   // 95 and 77), and else two steps' loads are under way (32 of 4096 x 7168, 32 rows: 406
   // us, with one 445; where the weights are read across 492 and 402).
-  if (E * ((mean + 127) / 128) * ((N + 127) / 128) <= 192 || (QT && mean <= 24))
+  const int64_t tiles = E * ((mean + 127) / 128) * ((N + 127) / 128);
+  if (tiles <= 192 || (tiles <= 256 && K >= 1536) || (QT && mean <= 24))
     return product_tiles<128, 128, 2, 2, 1, 2, QT>(rows, r_cap, K, weight, E, N, counts, offsets, entries, out, s);
   return product_tiles<128, 128, 2, 2, QT ? 1 : 2, 1, QT>(rows, r_cap, K, weight, E, N, counts, offsets, entries, out, s);
 }
@@ -597,11 +598,14 @@ int32_t wgrad_tiles(const uint16_t* dout, const uint16_t* rows, int64_t width, i
   return launch_status();
 }
 
-// Into how many shares an expert's rows are cut (by the mean): where 128 x 128 tiles
-// are fewer than two a CU, as many as make up for it, each of 256 rows at least.
+// Into how many shares an expert's rows are cut (by the mean): where 128 x 128 tiles are
+// fewer than two a CU (four where the shares are small to store), as many as make up for
+// it, each of 256 (128) rows at least.  2 experts of 512 x 512, 8192 rows each: 107 us
+// whole, 25 in 16 shares.
 int wgrad_parts(int64_t width, int64_t hidden, int64_t E, int64_t entries) {
   const int64_t tiles = E * ((width + 127) / 128) * ((hidden + 127) / 128);
-  int64_t parts = 512 / tiles, most = entries / E / 256;
+  const int64_t more = E * width * hidden <= (1 << 22) ? 2 : 1;
+  int64_t parts = more * 512 / tiles, most = more * entries / E / 256;
   parts = parts < most ? parts : most;
   return (int)(parts < 2 ? 1 : parts > 16 ? 16 : parts);
 }

@@ -33,6 +33,7 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int c) {
 // SB scale bytes.
 template <int C, int THREADS, int RB, int SB>
 struct MxTile {
+  int tid;  // of the THREADS that share the tile
   static constexpr int kRowPieces = RB / 16, kPieces = C * kRowPieces / THREADS;
   static constexpr int kWords = C * SB / 4, kSc = (kWords + THREADS - 1) / THREADS;
   static constexpr int kBytes = C * (RB + SB);
@@ -40,15 +41,16 @@ struct MxTile {
   u32x4 v[kPieces];
   uint32_t sv[kSc];
 
-  __device__ __forceinline__ void init(int64_t row_bytes, int64_t row_blocks, int c_n) {
+  __device__ __forceinline__ void init(int thread, int64_t row_bytes, int64_t row_blocks, int c_n) {
+    tid = thread;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int p = threadIdx.x + i * THREADS;
+      const int p = tid + i * THREADS;
       off[i] = (uint32_t)(min(p / kRowPieces, c_n - 1) * (uint32_t)row_bytes + 16 * (p % kRowPieces));
     }
 #pragma unroll
     for (int i = 0; i < kSc; ++i) {
-      const int p = min((int)threadIdx.x + i * THREADS, kWords - 1);
+      const int p = min(tid + i * THREADS, kWords - 1);
       soff[i] = (uint32_t)(min(p / (SB / 4), c_n - 1) * (uint32_t)row_blocks + 4 * (p % (SB / 4)));
     }
   }
@@ -56,7 +58,7 @@ struct MxTile {
   // past it are zeros.
   template <bool EDGE>
   __device__ __forceinline__ void load_piece(int i, const uint8_t* codes, int bytes) {
-    const int p = threadIdx.x + i * THREADS;
+    const int p = tid + i * THREADS;
     if (!EDGE || 16 * (p % kRowPieces) < bytes) v[i] = ld_any<u32x4>(codes + off[i]);
     else v[i] = u32x4{0u, 0u, 0u, 0u};
   }
@@ -68,7 +70,7 @@ struct MxTile {
         sv[i] = ld_any<uint32_t>(scales + soff[i]);
         continue;
       }
-      const int p = min((int)threadIdx.x + i * THREADS, kWords - 1), n = blocks - 4 * (p % (SB / 4));
+      const int p = min(tid + i * THREADS, kWords - 1), n = blocks - 4 * (p % (SB / 4));
       sv[i] = 0;
 #pragma unroll
       for (int b = 0; b < 4; ++b)
@@ -82,14 +84,21 @@ struct MxTile {
     load_scales<EDGE>(scales, blocks);
   }
   __device__ __forceinline__ void store_piece(int i, char* lds) const {
-    const int p = threadIdx.x + i * THREADS;
+    const int p = tid + i * THREADS;
     *reinterpret_cast<u32x4*>(lds + chunk_at<RB>(p / kRowPieces, p % kRowPieces)) = v[i];
   }
+  // Eight scale bytes of a row (two lanes' words) are stored as 0, 4, 1, 5, 2, 6, 3, 7,
+  // so that one 16-bit read has a lane group's blocks of both halves of a step.
   __device__ __forceinline__ void store_scales(char* lds) const {
 #pragma unroll
     for (int i = 0; i < kSc; ++i) {
-      const int p = threadIdx.x + i * THREADS;
-      if (kWords % THREADS == 0 || p < kWords) *reinterpret_cast<uint32_t*>(lds + C * RB + 4 * p) = sv[i];
+      const int p = tid + i * THREADS;
+      uint32_t w = sv[i];
+      if (SB == 8) {
+        const uint32_t o = lane_xor1(w), lo = p & 1 ? o : w, hi = p & 1 ? w : o;
+        w = __builtin_amdgcn_perm(hi, lo, p & 1 ? 0x07030602u : 0x05010400u);
+      }
+      if (kWords % THREADS == 0 || p < kWords) *reinterpret_cast<uint32_t*>(lds + C * RB + 4 * p) = w;
     }
   }
   __device__ __forceinline__ void store(char* lds) const {
@@ -100,15 +109,16 @@ struct MxTile {
 };
 
 // One output tile of BM x BN per workgroup, 256 values (MXFP8 rows: 128) a step
-// through two LDS buffers.
-template <int BM, int BN, int WM, int WN, bool A8>
+// through two LDS buffers.  SHARES groups of WM x WN waves take the steps in turn, each
+// through buffers of its own; the first ends with the sum.
+template <int BM, int BN, int WM, int WN, int SHARES, bool A8>
 struct MxProduct {
   static constexpr int kThreads = 64 * WM * WN, MT = BM / WM / 16, NT = BN / WN / 16;
   static constexpr int kStep = A8 ? 128 : 256, SB = kStep / 32, kRowW = kStep / 2;
   typedef MxTile<BM, kThreads, 128, SB> TileA;
   typedef MxTile<BN, kThreads, kRowW, SB> TileW;
   static constexpr int kBuf = TileA::kBytes + TileW::kBytes;
-  static constexpr int kOut = WM * WN * MT * 2048, kLds = 2 * kBuf > kOut ? 2 * kBuf : kOut;
+  static constexpr int kOut = WM * WN * MT * 2048, kAll = 2 * SHARES * kBuf, kLds = kAll > kOut ? kAll : kOut;
   f32x4 acc[MT][NT];
 
   // A step's products in kParts parts, `between(part)` called before each: the lanes'
@@ -149,18 +159,18 @@ struct MxProduct {
           acc[c][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(w[i], none), a, acc[c][i], kE2M1, kE4M3, 0,
                                                                        sw[i], 0, sa[c]);
       } else {
-        // which blocks of 32 a lane group takes is free: 2 g in the first half, 2 g + 1
-        // in the second, so that one 16-bit read has both scales
+        // lane group g: values 32 g .. + 31 of the step's first half, then of its second
+        // (neighbouring chunks: groups that took every other one would meet in LDS's banks)
         constexpr int S = c / 4, J = MT / 4;
         if constexpr (c % 4 == 0) {
 #pragma unroll
           for (int i = 0; i < NT; ++i)
-            w[i] = *reinterpret_cast<const u32x4*>(w_lds + chunk_at<kRowW>(16 * (wn * NT + i) + r, 2 * g + S));
+            w[i] = *reinterpret_cast<const u32x4*>(w_lds + chunk_at<kRowW>(16 * (wn * NT + i) + r, 4 * S + g));
         }
         between(part);
 #pragma unroll
         for (int j = c % 4 * J; j < (c % 4 + 1) * J; ++j) {
-          const u32x4 a = *reinterpret_cast<const u32x4*>(a_lds + chunk_at<128>(16 * (wm * MT + j) + r, 2 * g + S));
+          const u32x4 a = *reinterpret_cast<const u32x4*>(a_lds + chunk_at<128>(16 * (wm * MT + j) + r, 4 * S + g));
 #pragma unroll
           for (int i = 0; i < NT; ++i)
             acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(w[i], none), wide(a, none), acc[j][i], kE2M1,
@@ -170,9 +180,12 @@ struct MxProduct {
     });
   }
 
-  __device__ __forceinline__ void run(char* lds, const uint8_t* a, const uint8_t* as, int a_n, const uint8_t* w,
+  __device__ __forceinline__ void run(char* all_lds, const uint8_t* a, const uint8_t* as, int a_n, const uint8_t* w,
                                       const uint8_t* ws, int w_n, int K) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave / WN, wn = wave % WN;
+    const int share = SHARES == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
+    const int tid = threadIdx.x - share * kThreads;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
+    char* lds = all_lds + share * 2 * kBuf;
 #pragma unroll
     for (int j = 0; j < MT; ++j)
 #pragma unroll
@@ -180,17 +193,24 @@ struct MxProduct {
     if (K <= 0) return;
     TileA ta;
     TileW tw;
-    ta.init(A8 ? K : K / 2, K / 32, a_n);
-    tw.init(K / 2, K / 32, w_n);
-    int left = K;
+    ta.init(tid, A8 ? K : K / 2, K / 32, a_n);
+    tw.init(tid, K / 2, K / 32, w_n);
+    const int all = (K + kStep - 1) / kStep, steps = (all + SHARES - 1) / SHARES;
+    const int mine = (all - share + SHARES - 1) / SHARES;  // steps of this group; the first has `steps`
+    int left = K - share * kStep;  // from this group's next step on: values that are not loaded yet
+    a += share * 128;
+    as += share * SB;
+    w += share * kRowW;
+    ws += share * SB;
     auto advance = [&]() {
-      a += 128;
-      as += SB;
-      w += kRowW;
-      ws += SB;
-      left -= kStep;
+      a += SHARES * 128;
+      as += SHARES * SB;
+      w += SHARES * kRowW;
+      ws += SHARES * SB;
+      left -= SHARES * kStep;
     };
     auto load = [&]() {
+      if (left <= 0) return;
       if (left >= kStep) {
         ta.template load<false>(a, as, 0, 0);
         tw.template load<false>(w, ws, 0, 0);
@@ -201,15 +221,16 @@ struct MxProduct {
       advance();
     };
     load();
-    ta.store(lds);
-    tw.store(lds + TileA::kBytes);
-    if (left > 0) load();
-    const int steps = (K + kStep - 1) / kStep;
+    if (mine > 0) {
+      ta.store(lds);
+      tw.store(lds + TileA::kBytes);
+    }
+    load();
     __syncthreads();
     // The steps whose loads (two steps ahead) are whole: the next step's values on their
     // way to LDS and the one after's to the registers they leave, between the products.
     int t = 0;
-    for (; t < K / kStep - 2; ++t) {
+    for (; t < K / kStep / SHARES - 2; ++t) {  // as many for each group
       const char* cur = lds + ((t & 1) ? kBuf : 0);
       char* next = lds + ((t & 1) ? 0 : kBuf);
       compute(cur, cur + TileA::kBytes, wm, wn, [&](auto part) {
@@ -237,24 +258,28 @@ struct MxProduct {
     for (; t < steps; ++t) {
       const char* cur = lds + ((t & 1) ? kBuf : 0);
       char* next = lds + ((t & 1) ? 0 : kBuf);
-      if (t + 1 < steps) {
+      if (t + 1 < mine) {
         ta.store(next);
         tw.store(next + TileA::kBytes);
-        if (left > 0) load();
+        load();
       }
-      compute(cur, cur + TileA::kBytes, wm, wn, [](auto) {});
+      if (t < mine) compute(cur, cur + TileA::kBytes, wm, wn, [](auto) {});
       __syncthreads();
+    }
+    if constexpr (SHARES == 2) {  // the buffers are free
+      static_assert(kLds >= BM * BN * 4, "the sums fit the buffers");
+      join_shares(acc, all_lds, tid, share);
     }
   }
 };
 
-template <int BM, int BN, int WM, int WN, bool A8>
-__global__ __launch_bounds__(64 * WM * WN) void k_mxfp4_grouped_gemm(const uint8_t* __restrict__ data,
+template <int BM, int BN, int WM, int WN, int SHARES, bool A8>
+__global__ __launch_bounds__(64 * WM * WN * SHARES) void k_mxfp4_grouped_gemm(const uint8_t* __restrict__ data,
                                                                      const uint8_t* __restrict__ scales, int K,
                                                                      const uint8_t* __restrict__ wcodes,
                                                                      const uint8_t* __restrict__ wscales, int64_t N,
                                                                      Groups gr, uint16_t* __restrict__ out) {
-  typedef MxProduct<BM, BN, WM, WN, A8> P;
+  typedef MxProduct<BM, BN, WM, WN, SHARES, A8> P;
   extern __shared__ char lds[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave / WN, wn = wave % WN;
   Span s;
@@ -269,9 +294,10 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mxfp4_grouped_gemm(const uint8
   else
     prod.run(lds, data, scales, 1, wcodes, wscales, 1, 0);
   static_assert(P::NT == 4, "a wave stores 64 columns");
-  const int m = wm * P::MT * 16, n = n0 + wn * 64;
   if (s.extent > BM)
-    clear_rows(out + (int64_t)s.row0 * N + n0, N, BM, s.extent, (int)min((int64_t)BN, N - n0));
+    clear_rows(out + row * N + n0, N, BM, s.extent, (int)min((int64_t)BN, N - n0));
+  if (wave >= WM * WN) return;
+  const int m = wm * P::MT * 16, n = n0 + wn * 64;
   store_block64<P::MT>(prod.acc, lds + wave * P::MT * 2048, out + (row + m) * N + n, N, s.used - m, s.extent - m,
                        (int)min((int64_t)64, N - n));
 }
@@ -402,15 +428,15 @@ __global__ __launch_bounds__(NT == 1 ? 512 : 256) void k_mxfp4_grouped_few(
 using namespace mtb;
 
 namespace {
-template <int BM, int BN, int WM, int WN, bool A8>
+template <int BM, int BN, int WM, int WN, int SHARES, bool A8>
 int32_t mx_tiles(const uint8_t* data, const uint8_t* scales, int64_t r_cap, int64_t K, const uint8_t* wcodes,
                    const uint8_t* wscales, int64_t E, int64_t N, const int32_t* counts, const int32_t* offsets,
                    int64_t entries, uint16_t* out, hipStream_t s) {
   const Groups gr{counts, offsets, (int)E, (int)r_cap};
   const int64_t blocks = span_blocks(r_cap, E, !counts, entries, BM, (N + BN - 1) / BN);
   if (blocks >= kSizeLimit) return EP_ERR_RANGE;
-  const size_t lds = MxProduct<BM, BN, WM, WN, A8>::kLds;
-  hipLaunchKernelGGL((k_mxfp4_grouped_gemm<BM, BN, WM, WN, A8>), dim3((unsigned)blocks), dim3(64 * WM * WN), lds, s, data,
+  const size_t lds = MxProduct<BM, BN, WM, WN, SHARES, A8>::kLds;
+  hipLaunchKernelGGL((k_mxfp4_grouped_gemm<BM, BN, WM, WN, SHARES, A8>), dim3((unsigned)blocks), dim3(64 * WM * WN * SHARES), lds, s, data,
                      scales, (int)K, wcodes, wscales, N, gr, out);
   return launch_status();
 }
@@ -449,8 +475,11 @@ int32_t mx_product(const uint8_t* data, const uint8_t* scales, int64_t r_cap, in
   // experts of 4096 x 4096, 259 rows each (256 tiles), 40 us, by small ones 52; 128 rows
   // each 35 and 31; 4 experts of 1024 x 2048, 512 rows each (32 tiles), 22 and 13.
   if (mean >= 192 && E * ((mean + 255) / 256) * ((N + 255) / 256) >= 112)
-    return mx_tiles<256, 256, 2, 4, A8>(data, scales, r_cap, K, wcodes, wscales, E, N, counts, offsets, entries, out, s);
-  return mx_tiles<128, 128, 2, 2, A8>(data, scales, r_cap, K, wcodes, wscales, E, N, counts, offsets, entries, out, s);
+    return mx_tiles<256, 256, 2, 4, 1, A8>(data, scales, r_cap, K, wcodes, wscales, E, N, counts, offsets, entries, out, s);
+  // Small ones: where they are fewer than the CUs two groups of waves share the sum.
+  if (E * ((mean + 127) / 128) * ((N + 127) / 128) <= 192)
+    return mx_tiles<128, 128, 2, 2, 2, A8>(data, scales, r_cap, K, wcodes, wscales, E, N, counts, offsets, entries, out, s);
+  return mx_tiles<128, 128, 2, 2, 1, A8>(data, scales, r_cap, K, wcodes, wscales, E, N, counts, offsets, entries, out, s);
 }
 }  // namespace
 

@@ -206,20 +206,28 @@ __global__ __launch_bounds__(THREADS) void k_drmsnorm(const uint16_t* __restrict
   }
 }
 
-// dw = the sum of the parts, 16 threads a column, each its run of them in order.
+// dw = the sum of the parts, 32 threads a column, each its run of them in order, eight
+// loads at a time.
 __global__ __launch_bounds__(1024) void k_drmsnorm_weight(const float* __restrict__ part, int parts, int H,
                                                           float* __restrict__ dw) {
-  __shared__ float s[16][64];
-  const int c = blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
-  const int each = (parts + 15) >> 4, lo = q * each, hi = min(parts, lo + each);
+  __shared__ float s[32][33];
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), q = threadIdx.x >> 5;  // H is a multiple of 32
+  const int each = (parts + 31) >> 5, lo = q * each, hi = min(parts, lo + each);
   float v = 0.0f;
-  if (c < H)
-    for (int p = lo; p < hi; ++p) v += part[(int64_t)p * H + c];
-  s[q][threadIdx.x & 63] = v;
-  __syncthreads();
-  if (q || c >= H) return;
+  int p = lo;
+  for (; p + 8 <= hi; p += 8) {
+    float a[8];
 #pragma unroll
-  for (int i = 1; i < 16; ++i) v += s[i][threadIdx.x];
+    for (int i = 0; i < 8; ++i) a[i] = part[(int64_t)(p + i) * H + c];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v += a[i];
+  }
+  for (; p < hi; ++p) v += part[(int64_t)p * H + c];
+  s[q][threadIdx.x & 31] = v;
+  __syncthreads();
+  if (q) return;
+#pragma unroll
+  for (int i = 1; i < 32; ++i) v += s[i][threadIdx.x];
   dw[c] = v;
 }
 
@@ -305,7 +313,7 @@ MTB_EXPORT int32_t drmsnorm(const uint16_t* dy, const uint16_t* h, const uint16_
                            rstd, dh, (int)rows, (int)hidden, dx, part);
     });
   if (parts == 1) return launch_status();
-  hipLaunchKernelGGL(k_drmsnorm_weight, dim3((unsigned)((hidden + 63) / 64)), dim3(1024), 0, (hipStream_t)stream,
+  hipLaunchKernelGGL(k_drmsnorm_weight, dim3((unsigned)(hidden / 32)), dim3(1024), 0, (hipStream_t)stream,
                      (const float*)workspace, parts, (int)hidden, dweight);
   return launch_status();
 }
