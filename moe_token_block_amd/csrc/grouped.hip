@@ -110,36 +110,35 @@ struct Product {
   typedef Tile<BM, kThreads, PT, SETS> TileP;
   typedef Tile<BN, kThreads, QT, SETS> TileQ;
   static_assert(TileP::kPieces + TileQ::kPieces == 8, "a piece for each of a step's eight parts");
-  
-  static constexpr bool GROUPED = !PT && !QT && BM == 256;
   static constexpr int kBuf = (BM + BN) * 128, kLds = 2 * SHARES * kBuf;
   f32x4 acc[MT][NT];
 
-  // A step's products in eight parts, `between(part)` called in each.  GROUP: a part's
-  // reads, store, load and products are kept together (131072 rows, 7168 x 4096: 7.00 ->
-  // 6.84 ms; where an operand is read across, or with small tiles, it costs 2 to 20%).
-  template <bool GROUP, typename F>
+  // A step's products in eight parts, `between(part)` called in each.  The next part's
+  // operands are read before it: no LDS read moves ahead of the stores in `between`.
+  template <typename F>
   __device__ __forceinline__ void compute(const char* buf, int wm, int wn, F&& between) {
-    bf16x8 b[NT];
-    static_for<0, 8>([&](auto part) {
-      constexpr int c = decltype(part)::value, ks = c / 4, jg = c % 4, J = MT / 4;
+    constexpr int J = MT / 4;
+    bf16x8 b[2][NT], a[2][J];
+    auto read = [&](auto part) {
+      constexpr int c = decltype(part)::value, ks = c / 4, jg = c % 4;
       if constexpr (jg == 0) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) b[i] = TileQ::frag(buf + BM * 128, 16 * (wn * NT + i), ks);
+        for (int i = 0; i < NT; ++i) b[ks][i] = TileQ::frag(buf + BM * 128, 16 * (wn * NT + i), ks);
       }
+#pragma unroll
+      for (int j = 0; j < J; ++j) a[c & 1][j] = TileP::frag(buf, 16 * (wm * MT + jg * J + j), ks);
+    };
+    read(std::integral_constant<int, 0>{});
+    static_for<0, 8>([&](auto part) {
+      constexpr int c = decltype(part)::value, ks = c / 4, jg = c % 4;
+      if constexpr (c < 7) read(std::integral_constant<int, c + 1>{});
       between(part);
 #pragma unroll
-      for (int j = jg * J; j < (jg + 1) * J; ++j) {
-        const bf16x8 a = TileP::frag(buf, 16 * (wm * MT + j), ks);
+      for (int j = 0; j < J; ++j)
 #pragma unroll
-        for (int i = 0; i < NT; ++i) acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[i], a, acc[j][i], 0, 0, 0);
-      }
-      if constexpr (GROUP) {
-        __builtin_amdgcn_sched_group_barrier(0x100, J + (jg == 0 ? (QT ? 2 : 1) * NT : 0), 0);
-        __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x8, NT * J, 0);
-      }
+        for (int i = 0; i < NT; ++i)
+          acc[jg * J + j][i] =
+              __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[ks][i], a[c & 1][j], acc[jg * J + j][i], 0, 0, 0);
     });
   }
 
@@ -196,7 +195,7 @@ struct Product {
         constexpr int set = decltype(sub)::value;
         const char* cur = lds + (((t + set) & 1) ? kBuf : 0);
         char* next = lds + (((t + set) & 1) ? 0 : kBuf);
-        compute<GROUPED>(cur, wm, wn, [&](auto part) {
+        compute(cur, wm, wn, [&](auto part) {
           constexpr int c = decltype(part)::value;
           if constexpr (c < TileP::kPieces) {
             tp.store_piece(set, c, next);
@@ -221,7 +220,7 @@ struct Product {
           tq.store(set, next + BM * 128);
           load(set);
         }
-        if (t + set < mine) compute<false>(cur, wm, wn, [](auto) {});
+        if (t + set < mine) compute(cur, wm, wn, [](auto) {});
         __syncthreads();
       });
     }
@@ -605,7 +604,7 @@ int32_t wgrad_tiles(const uint16_t* dout, const uint16_t* rows, int64_t width, i
 int wgrad_parts(int64_t width, int64_t hidden, int64_t E, int64_t entries) {
   const int64_t tiles = E * ((width + 127) / 128) * ((hidden + 127) / 128);
   const int64_t more = E * width * hidden <= (1 << 22) ? 2 : 1;
-  int64_t parts = more * 512 / tiles, most = more * entries / E / 256;
+  int64_t parts = more * 512 / tiles, most = more * (entries / E) / 256;
   parts = parts < most ? parts : most;
   return (int)(parts < 2 ? 1 : parts > 16 ? 16 : parts);
 }
@@ -622,7 +621,8 @@ int32_t wgrad(const uint16_t* dout, const uint16_t* rows, int64_t width, int64_t
     return launch_status();
   }
   // Large tiles where they are as many as the CUs: 8 experts of 4096 x 4096 (2048 tiles),
-  // 512 rows each, 175 us, by small ones 234; 32 of 512 x 512 (128), 4096 rows, 105 and 97.
+  // 512 rows each, 175 us, by small ones 234; 32 of 512 x 512 (128), 4096 rows, 105 and 97;
+  // 4 of 1024 x 2048 (128), 2048 rows, 55 (57 in two shares) and 45.
   if (gr.experts * ((width + 255) / 256) * ((hidden + 255) / 256) >= 256)
     return wgrad_tiles<256, 256, 2, 4, 1, 1>(dout, rows, width, hidden, gr, 1, out, s);
   return wgrad_tiles<128, 128, 2, 2, 2, 1>(dout, rows, width, hidden, gr, 1, out, s);
