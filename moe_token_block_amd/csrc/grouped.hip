@@ -425,6 +425,10 @@ __global__ __launch_bounds__(512) void k_bf16_grouped_few_across(const uint16_t*
   }
 }
 
+// Tiles of one expert's share that one XCD takes: as many as run there at once.
+template <int BM>
+constexpr int kWholeOnXcd = BM == 256 ? 32 : 64;
+
 // dW of one expert, or one of `parts` shares of it (the rows' steps of 64 taken in
 // equal runs; FP32, share i at out + i * E * N * K): P dout's columns, Q the rows'.
 template <int BM, int BN, int WM, int WN, int SETS, int SHARES, typename OUT>
@@ -435,13 +439,22 @@ __global__ __launch_bounds__(64 * WM * WN * SHARES) void k_bf16_grouped_wgrad(co
   extern __shared__ char lds[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave / WN, wn = wave % WN;
   const int tm = (int)((N + BM - 1) / BM), tn = (int)((K + BN - 1) / BN);
-  // Every XCD takes a run of each share's tiles: experts differ in their rows, and a run
-  // of whole experts would leave most XCDs idle (16 experts of 1592 x 3304, loads by
-  // 1 / rank^1.2: 585 -> 199 us).
-  const int chunk = (tm * tn + 7) >> 3, at = (int)(blockIdx.x >> 3), group = at / chunk;
-  const int part = group / gr.experts, e = group - part * gr.experts;
-  const int id = (int)((blockIdx.x + group + part) & 7) * chunk + at - group * chunk;  // few tiles: not always the same XCDs
-  if (id >= tm * tn) return;
+  const int per = tm * tn, x = (int)(blockIdx.x & 7), at = (int)(blockIdx.x >> 3);  // x: the XCD
+  int group, id;  // which share of which expert, and which of its tiles
+  if (per <= kWholeOnXcd<BM>) {
+    // all on one XCD, whose L2 then reads the share's rows once (32 experts of 512 x 512,
+    // 4096 rows: 97 us, spread 130); an expert's shares on one after the other
+    group = at / per * 8 + x;
+    id = at % per;
+  } else {
+    // a run on each: experts differ in their rows, and whole ones would leave most XCDs
+    // idle (16 of 1592 x 3304, loads by 1 / rank^1.2: 585 -> 199 us)
+    const int run = (per + 7) >> 3;
+    group = at / run;
+    id = x * run + at % run;
+  }
+  if (group >= parts * gr.experts || id >= per) return;
+  const int e = group / parts, part = group - e * parts;
   int i, j;
   banded(id, tm, tn, i, j);
   const int m0 = i * BM, n0 = j * BN;
@@ -457,7 +470,7 @@ __global__ __launch_bounds__(64 * WM * WN * SHARES) void k_bf16_grouped_wgrad(co
            (int)min((int64_t)BN, K - n0), cnt);
   if (wave >= WM * WN) return;
   const int m = m0 + wm * P::MT * 16, n = n0 + wn * 64;
-  OUT* o = out + ((int64_t)group * N + m) * K + n;
+  OUT* o = out + (((int64_t)part * gr.experts + e) * N + m) * K + n;
   const int rest = (int)(N - m), cols = (int)min((int64_t)64, K - n);
   if constexpr (sizeof(OUT) == 2) store_block64<P::MT>(prod.acc, lds + wave * P::MT * 2048, o, K, rest, rest, cols);
   else store_block64<P::MT>(prod.acc, lds + wave * P::MT * 2048, o, K, rest, cols);
@@ -589,7 +602,8 @@ int32_t product(const uint16_t* rows, int64_t r_cap, int64_t K, const uint16_t* 
 template <int BM, int BN, int WM, int WN, int SETS, int SHARES, typename OUT>
 int32_t wgrad_tiles(const uint16_t* dout, const uint16_t* rows, int64_t width, int64_t hidden, const Groups& gr, int parts,
                     OUT* out, hipStream_t s) {
-  const int64_t tiles = ((width + BM - 1) / BM) * ((hidden + BN - 1) / BN), blocks = parts * gr.experts * ((tiles + 7) / 8 * 8);
+  const int64_t per = ((width + BM - 1) / BM) * ((hidden + BN - 1) / BN), groups = (int64_t)parts * gr.experts;
+  const int64_t blocks = per <= kWholeOnXcd<BM> ? (groups + 7) / 8 * 8 * per : groups * ((per + 7) / 8 * 8);
   if (blocks >= kSizeLimit) return EP_ERR_RANGE;
   const size_t lds = Product<BM, BN, WM, WN, true, true, SETS, SHARES>::kLds;
   hipLaunchKernelGGL((k_bf16_grouped_wgrad<BM, BN, WM, WN, SETS, SHARES, OUT>), dim3((unsigned)blocks), dim3(64 * WM * WN * SHARES), lds, s, dout,
@@ -603,7 +617,7 @@ int32_t wgrad_tiles(const uint16_t* dout, const uint16_t* rows, int64_t width, i
 // whole, 25 in 16 shares.
 int wgrad_parts(int64_t width, int64_t hidden, int64_t E, int64_t entries) {
   const int64_t tiles = E * ((width + 127) / 128) * ((hidden + 127) / 128);
-  const int64_t more = E * width * hidden <= (1 << 22) ? 2 : 1;
+  const int64_t more = E * width * hidden <= (1 << 20) ? 2 : 1;
   int64_t parts = more * 512 / tiles, most = more * (entries / E) / 256;
   parts = parts < most ? parts : most;
   return (int)(parts < 2 ? 1 : parts > 16 ? 16 : parts);
@@ -614,7 +628,7 @@ int32_t wgrad(const uint16_t* dout, const uint16_t* rows, int64_t width, int64_t
               OUT* out, float* workspace, hipStream_t s) {
   const int parts = wgrad_parts(width, hidden, gr.experts, entries);
   if (parts > 1) {
-    const int32_t st = wgrad_tiles<128, 128, 2, 2, 2, 1>(dout, rows, width, hidden, gr, parts, workspace, s);
+    const int32_t st = wgrad_tiles<128, 128, 2, 2, 1, 1>(dout, rows, width, hidden, gr, parts, workspace, s);
     if (st != EP_OK) return st;
     const int64_t n = gr.experts * width * hidden;
     hipLaunchKernelGGL(k_wgrad_join<OUT>, dim3((unsigned)((n + 1023) / 1024)), dim3(256), 0, s, workspace, parts, n, out);
@@ -625,7 +639,7 @@ int32_t wgrad(const uint16_t* dout, const uint16_t* rows, int64_t width, int64_t
   // 4 of 1024 x 2048 (128), 2048 rows, 55 (57 in two shares) and 45.
   if (gr.experts * ((width + 255) / 256) * ((hidden + 255) / 256) >= 256)
     return wgrad_tiles<256, 256, 2, 4, 1, 1>(dout, rows, width, hidden, gr, 1, out, s);
-  return wgrad_tiles<128, 128, 2, 2, 2, 1>(dout, rows, width, hidden, gr, 1, out, s);
+  return wgrad_tiles<128, 128, 2, 2, 1, 1>(dout, rows, width, hidden, gr, 1, out, s);
 }
 
 }  // namespace
