@@ -27,7 +27,8 @@
  *   - Errors that only the data can reveal (an expert id out of range) are
  *     reported by setting a caller-provided device word `d_error` to a
  *     non-zero EP_DEVERR_* bit; the offending entry is dropped.
- *   - Calls that share output buffers must not overlap in time.
+ *   - Calls that share output buffers or a workspace must not overlap in time.
+ *   - Outputs must not overlap inputs, but where a function says so.
  *
  * Formats (fixed by this library's readings of the pages; see each function):
  *   E2M1  4-bit code: bit 3 sign, bits 0..2 index into {0,.5,1,1.5,2,3,4,6};

@@ -8,7 +8,19 @@
 // The three differ in how an operand lies in memory: along the sum ("R": a tile
 // row is 64 values of one output row or column), or across it ("T": a tile row is
 // one term of the sum for all of the tile's output rows or columns), which LDS's
-// transposing read turns into the instruction's operand.
+// transposing read turns into the instruction's operand.  For few rows the weights'
+// bytes are the time, and kernels of their own stream them.
+//
+// Measured (large library products of the same kinds reach 1430, 1250 and 1100
+// TFLOP/s): 131072 rows of 32 experts, 7168 x 4096, 6.6 to 6.9 ms, 1120 to 1170
+// TFLOP/s; the rows' gradient of 8192 uneven rows, 8 experts of 4096 x 4096, 312 us,
+// 880; the weights' of 65536 rows, 16 experts of 4096 x 4096, 1.79 to 1.88 ms, 1170 to
+// 1230.  The matrix unit is busy about half of the time; the rest are the steps'
+// barriers with the first LDS reads behind them, and the first loads and the stores of
+// a tile, which nothing else on the CU overlaps (128 KB of LDS, 240 registers a lane).
+// Measured without gain: a second barrier a step that lets the next step's operands be
+// read ahead (8% slower), tiles of 256 x 128, raised wave priority, every load of a step
+// before its products (20% slower), four waves of 128 x 128 (they spill).
 #include "common.h"
 #include "grouped.h"
 #include "launch.h"
@@ -231,7 +243,8 @@ struct Product {
   }
 };
 
-// out[m, n] for grouped rows m: P the rows, Q the weights (QT: their transposes).
+// out[m, n] for grouped rows m: P the rows, Q the weights (QT: their transposes).  A tile
+// whose rows hold no entry, and those behind an expert's last, are cleared.
 template <int BM, int BN, int WM, int WN, int SETS, int SHARES, bool QT>
 __global__ __launch_bounds__(64 * WM * WN * SHARES) void k_bf16_grouped_gemm(const uint16_t* __restrict__ rows, int64_t K,
                                                                     const uint16_t* __restrict__ weight, int64_t N,
@@ -262,10 +275,13 @@ __global__ __launch_bounds__(64 * WM * WN * SHARES) void k_bf16_grouped_gemm(con
 
 // out[m, n] for experts with few rows, where the time is that of reading the weights.
 // A workgroup takes 16 RT weight rows of one expert and 16 NT of its rows at a time (the
-// z-th of gridDim.z first, then every gridDim.z-th); its waves take the sum's steps of 128 terms in turn and join their sums
-// through LDS.  Weights and rows go from memory to registers, four lanes on 64
-// contiguous bytes, and are brought into the instruction's order within lane quads;
-// a step's loads are in flight while the step before is multiplied.
+// z-th of gridDim.z first, then every gridDim.z-th); its waves take the sum's steps of
+// 128 terms in turn and join their sums through LDS.  Weights and rows go from memory to
+// registers, four lanes on 64 contiguous bytes (a lane a row costs the L1 four times the
+// accesses), and are brought into the instruction's order within lane quads; a step's
+// loads are in flight while the step before is multiplied.  One token, 2 of 8 experts of
+// 4096 x 4096: 14 us for 68 MB (4.8 TB/s; the first loads' latency and the join are a
+// third); 128 rows of 32 experts of 4096 x 7168: 307 us for 1.88 GB (6.1 TB/s).
 template <int RT, int NT>
 __global__ __launch_bounds__(NT == 1 ? 512 : 256) void k_bf16_grouped_few(const uint16_t* __restrict__ rows, int64_t K,
                                                           const uint16_t* __restrict__ weight, int64_t N, Groups gr,
@@ -354,7 +370,8 @@ __global__ __launch_bounds__(NT == 1 ? 512 : 256) void k_bf16_grouped_few(const 
 
 // drows for experts with few rows: as k_bf16_grouped_few, but the weights' rows are the
 // sum's terms: a wave's 64 of them by 64 columns go through LDS of its own, whose
-// transposing read makes the instruction's operand.
+// transposing read makes the instruction's operand.  One token, 2 of 8 experts of 4096 x
+// 2048: 16.5 us for 34 MB; 128 rows, 8 experts of 4096 x 4096: 63 us for 270 MB.
 template <int NT>
 __global__ __launch_bounds__(512) void k_bf16_grouped_few_across(const uint16_t* __restrict__ dout, int64_t N,
                                                                  const uint16_t* __restrict__ weight, int64_t K,
@@ -430,7 +447,9 @@ template <int BM>
 constexpr int kWholeOnXcd = BM == 256 ? 32 : 64;
 
 // dW of one expert, or one of `parts` shares of it (the rows' steps of 64 taken in
-// equal runs; FP32, share i at out + i * E * N * K): P dout's columns, Q the rows'.
+// equal runs; FP32, share i at out + i * E * N * K): P dout's columns, Q the rows'.  Short
+// sums are bound by a tile's fixed costs: 222 rows an expert, 32 of 2040 x 2440, 200 us
+// for 380 MB.
 template <int BM, int BN, int WM, int WN, int SETS, int SHARES, typename OUT>
 __global__ __launch_bounds__(64 * WM * WN * SHARES) void k_bf16_grouped_wgrad(const uint16_t* __restrict__ dout, int64_t N,
                                                                      const uint16_t* __restrict__ rows, int64_t K,

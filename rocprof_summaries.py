@@ -31,6 +31,9 @@ process itself never touches the GPU (every GPU run is a rocprofv3 child), but a
       marker kernels), and one run of the child without the profiler, which times the
       passes eager and in a graph -> profiles/kernel_times_expert_layer.md; for the NVFP4 products
       also three --pmc runs of it -> profiles/counters_expert_matvec.md.
+  python rocprof_summaries.py products [--raw DIR]
+      The same times of the grouped products and the norm, at the cases of
+      perf/more_operators.py -> profiles/kernel_times_products.md.
 """
 
 import argparse
@@ -350,11 +353,21 @@ def trace(args):
 
 
 # ------------------------------------------------------------------ the expert layer
-EXPERT_SOURCES = ("combine.hip", "common.h", "matvec.hip", "mxfp8.h", "swiglu.hip")
+EXPERT_SOURCES = ("combine.hip", "common.h", "matvec.hip", "mxfp8.h", "quad.h", "stream.h", "swiglu.hip")
 EXPERT_GROUPS = (("FETCH_SIZE",), ("TCC_REQ_sum", "TCC_MISS_sum", "TCC_EA0_RDREQ_DRAM_sum"),
                  ("SQ_INSTS_VALU", "SQ_ACTIVE_INST_VALU", "SQ_VALU_MFMA_BUSY_CYCLES", "SQ_BUSY_CU_CYCLES",
                   "SQ_INSTS_LDS", "SQ_LDS_BANK_CONFLICT", "SQ_WAIT_INST_ANY", "SQ_WAVE_CYCLES"))
 EXPERT_PASSES = 60
+
+
+PRODUCT_SOURCES = ("common.h", "grouped.h", "grouped.hip", "mxfp4.hip", "mxfp8.h", "mxgemm.hip", "norm.hip", "quad.h",
+                   "stream.h", "swiglu.hip")
+
+
+def product_cases():
+    """The cases of perf/more_operators.py."""
+    from perf import more_operators as ops
+    return ops, ops.listed()
 
 
 def expert_cases():
@@ -383,7 +396,7 @@ def expert_state(ops, case, seed):
 def expert_pass(args):
     """The profiled child: one case's passes between two marker kernels (digamma, used nowhere else)."""
     import torch
-    ops, cases = expert_cases()
+    ops, cases = product_cases() if args.products else expert_cases()
     ops.own = True
     case = next(c for c in cases if c["name"] == args.case)
     states = [expert_state(ops, case, seed) for seed in range(3)]
@@ -428,9 +441,9 @@ def expert_pass(args):
     print(json.dumps({"case": args.case, "us": us, "graph_us": graph_us, "loads": loads, **ops.work(case)}), flush=True)
 
 
-def _expert_run(tool, case, out, settle):
+def _expert_run(tool, case, out, settle, products=False):
     """One profiled run of the child; its line, the trace's directory and the command as shown."""
-    child = ["rocprof_summaries.py", "expert-pass", "--settle-s", str(settle)]
+    child = ["rocprof_summaries.py", "expert-pass", "--settle-s", str(settle)] + (["--products"] if products else [])
     tool = ["rocprofv3"] + tool + ["--output-format", "csv", "-d", "OUT", "-o", "run", "--"] if tool else []
     child += [] if tool else ["--timed"]
     text = run([out if a == "OUT" else a for a in tool] + [sys.executable, os.path.join(ROOT, child[0])] + child[1:]
@@ -445,21 +458,20 @@ def _between_marks(rows, name, order):
     return rows[marks[0] + 1:marks[-1]]
 
 
-def expert(args):
+def _times(args, raw, cases, sources, title, name, products=False):
+    """Traced and untraced times of the cases into profiles/NAME; the heading lines."""
     import hashlib
-    raw = args.raw or tempfile.mkdtemp(prefix="mtb_expert_")
-    _, cases = expert_cases()
     h = hashlib.sha256()
-    for f in EXPERT_SOURCES:
+    for f in sources:
         h.update(bench._code_only(open(os.path.join(ROOT, "moe_token_block_amd", "csrc", f)).read()).encode())
-    head = [f"Date {datetime.date.today().isoformat()}, `python rocprof_summaries.py expert`; sources "
-            f"({', '.join(EXPERT_SOURCES)}, code only) {h.hexdigest()[:16]}.  Commands (from the repository root, NAME "
+    head = [f"Date {datetime.date.today().isoformat()}, `python rocprof_summaries.py {args.what}`; sources "
+            f"({', '.join(sources)}, code only) {h.hexdigest()[:16]}.  Commands (from the repository root, NAME "
             "each case):", "", "```"]
     shown, md = [], []
     for c in cases:
         out = os.path.join(raw, "trace_" + c["name"])
-        plain, untraced = _expert_run([], c["name"], out, 0.3)
-        line, traced = _expert_run(["--kernel-trace"], c["name"], out, 0.3)
+        plain, untraced = _expert_run([], c["name"], out, 0.3, products)
+        line, traced = _expert_run(["--kernel-trace"], c["name"], out, 0.3, products)
         shown = [untraced, traced]
         rows = _between_marks(list(csv.DictReader(open(os.path.join(out, "run_kernel_trace.csv")))), "Kernel_Name",
                               lambda r: int(r["Start_Timestamp"]))
@@ -475,7 +487,7 @@ def expert(args):
                       f"{np.percentile(v, 25):.2f}-{np.percentile(v, 75):.2f} | {min(v):.2f} | "
                       + (f"{plain['us']:.2f} | {plain['graph_us']:.2f} | {line['bytes'] / 1e6:.1f} | "
                          f"{line['bytes'] / plain['graph_us'] / 1e6:.2f} |" if i == 0 else "| | | |"))
-    doc = ["# Times of the expert layer's calls", ""] + head + shown + ["```", "",
+    doc = [f"# {title}", ""] + head + shown + ["```", "",
            f"{EXPERT_PASSES} passes of each case over three input sets in turn, after 0.3 s of untimed passes.  Traced: "
            "duration of each of the call's kernels, start to end.  Untraced, per pass, the median of seven runs: the "
            "Python calls, and the same passes captured in one graph and replayed (no host time; a kernel's start "
@@ -483,8 +495,21 @@ def expert(args):
            "input and output once; TB/s: those over the time in a graph.", "",
            "| case | kernel | blocks of threads | traced median us | IQR us | min us | calls us | in a graph us | MB | TB/s |",
            "|---|---|---|---|---|---|---|---|---|---|"]
-    with open(os.path.join(args.out_dir, "kernel_times_expert_layer.md"), "w") as fh:
+    with open(os.path.join(args.out_dir, name), "w") as fh:
         fh.write("\n".join(doc + md) + "\n")
+    return head
+
+
+def products(args):
+    raw = args.raw or tempfile.mkdtemp(prefix="mtb_products_")
+    _times(args, raw, product_cases()[1], PRODUCT_SOURCES, "Times of the grouped products and of the norm",
+           "kernel_times_products.md", products=True)
+
+
+def expert(args):
+    raw = args.raw or tempfile.mkdtemp(prefix="mtb_expert_")
+    _, cases = expert_cases()
+    head = _times(args, raw, cases, EXPERT_SOURCES, "Times of the expert layer's calls", "kernel_times_expert_layer.md")
 
     ref = json.load(open(os.path.join(ROOT, "profiles", "counters.json")))["copy_reference"]
     shown, md = [], []
@@ -521,8 +546,9 @@ def expert(args):
 
 def main():
     p = argparse.ArgumentParser()
-    p.add_argument("what", choices=["counters", "kernels", "trace", "expert", "expert-pass"])
+    p.add_argument("what", choices=["counters", "kernels", "trace", "expert", "products", "expert-pass"])
     p.add_argument("--case", default=None, help="expert-pass: the case's name")
+    p.add_argument("--products", action="store_true", help="expert-pass: a case of perf/more_operators.py")
     p.add_argument("--timed", action="store_true", help="expert-pass: time the passes too, eager and in a graph")
     p.add_argument("--settle-s", type=float, default=0.0, help="expert-pass: seconds of passes before the recorded ones")
     p.add_argument("--workload", default="cfg3", choices=list(WORKLOAD_NAMES) + ["all"])
@@ -538,7 +564,7 @@ def main():
     if args.raw:
         args.raw = os.path.abspath(args.raw)
         os.makedirs(args.raw, exist_ok=True)
-    {"counters": counters, "kernels": kernel_times, "trace": trace, "expert": expert}[args.what](args)
+    {"counters": counters, "kernels": kernel_times, "trace": trace, "expert": expert, "products": products}[args.what](args)
 
 
 if __name__ == "__main__":
