@@ -474,7 +474,7 @@ int32_t mx_product(const uint8_t* data, const uint8_t* scales, int64_t r_cap, in
   // With more rows, too, where a long sum would be left to few tiles: a workgroup for
   // each 16 rows.
   constexpr int RT = A8 ? 1 : 2;
-  const int64_t chunks = (mean + 15) / 16;
+  const int64_t chunks = mean > 16 ? (mean + 15) / 16 : 1;  // without entries, too: the rows are cleared
   const bool thin = K > 2048 && E * ((N + 16 * RT - 1) / (16 * RT)) * chunks <= 2048 && chunks <= 65535;
   if ((mean <= 16 || thin) && groups <= 65535)
     return mx_few<RT, 1, A8>(data, scales, r_cap, K, wcodes, wscales, E, N, counts, offsets,

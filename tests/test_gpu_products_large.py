@@ -171,3 +171,22 @@ def test_a_workspace_of_ones_own(dev):
         mtb.ep_bf16_grouped_wgrad(d, x, plan, workspace=ws[:-1])
     with pytest.raises(mtb.EpError):
         mtb.ep_bf16_grouped_wgrad(d, x, plan, workspace=torch.zeros(need + 1, dtype=torch.uint8, device=dev)[1:])
+
+
+@pytest.mark.parametrize("room", [48, 300])
+def test_plans_without_entries(dev, room):
+    """No tokens at all, but grouped rows: zeros from every product."""
+    e, k, n = 3, 96, 40
+    plan = mtb.ep_route_plan(torch.zeros((0, 2), dtype=torch.int32, device=dev), e, 16, r_cap=room)
+    nan = lambda *s: torch.full(s, float("nan"), dtype=torch.bfloat16, device=dev)  # noqa: E731
+    u8 = lambda *s: torch.full(s, 255, dtype=torch.uint8, device=dev)  # noqa: E731
+    w = torch.ones((e, n, k), dtype=torch.bfloat16, device=dev)
+    wc, ws = (v.view(e, n, -1) for v in mtb.ep_mxfp4_pack(w.view(-1, k)))
+    for name, call in (("gemm", lambda: mtb.ep_bf16_grouped_gemm(nan(room, k), w, plan, out=nan(room, n))),
+                       ("dgrad", lambda: mtb.ep_bf16_grouped_dgrad(nan(room, n), w, plan, out=nan(room, k))),
+                       ("wgrad", lambda: mtb.ep_bf16_grouped_wgrad(nan(room, n), nan(room, k), plan, out=nan(e, n, k))),
+                       ("mx4", lambda: mtb.ep_mxfp4_grouped_gemm(u8(room, k // 2), u8(room, k // 32), wc, ws, plan, out=nan(room, n))),
+                       ("mx8", lambda: mtb.ep_mxfp4_grouped_gemm(u8(room, k), u8(room, k // 32), wc, ws, plan, out=nan(room, n)))):
+        print(name, flush=True)
+        got = call()
+        assert not bool(got.view(torch.int16).any()), name
