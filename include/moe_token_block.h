@@ -601,8 +601,10 @@ int32_t dswiglu_mxfp8_checkpoint(const uint8_t* data, const uint8_t* scales, con
  * no entry are not used; the first two write every row below r_cap that
  * the plan's spans cover or that lies behind them, zeros where there is no entry,
  * and the third writes every expert's weights, zeros for one without entries.
- *   hidden and width from 1 to 2^20, 1 <= num_experts <= 1024, r_cap < 2^25, and at
- *   most 2^31 output tiles, entries < 2^31 (EP_ERR_RANGE); no row needs an alignment.
+ *   hidden and width from 1 to 2^20, 1 <= num_experts <= 1024, r_cap < 2^25, entries <
+ *   2^31, and one grid for all output tiles (EP_ERR_RANGE): fewer than 2^23 of 128 x
+ *   128 fit, counting a row of them more for each expert and each 256 of r_cap; no row
+ *   needs an alignment.
  *   workspace of ep_bf16_grouped_wgrad_workspace_bytes(...) bytes, 16-byte aligned
  *   (EP_ERR_WORKSPACE; NULL where that is 0). */
 int32_t ep_bf16_grouped_gemm(const uint16_t* rows, int64_t r_cap, int64_t hidden, const uint16_t* weight,

@@ -114,6 +114,9 @@ inline int64_t span_blocks(int64_t r_cap, int64_t experts, bool dense, int64_t e
   return (tiles_m * tiles_n + 7) / 8 * 8;
 }
 
+// Whether `blocks` workgroups of `threads` make one grid (2^32 threads an axis do not).
+inline bool grid_fits(int64_t blocks, int threads) { return blocks < ((int64_t)1 << 32) / threads; }
+
 // Eight 16-bit values of which the first n exist.
 __device__ __forceinline__ u32x4 load8(const uint16_t* p, int n) {
   if (n >= 8) return ld_any<u32x4>(p);

@@ -530,7 +530,7 @@ int32_t check_sizes(int64_t r_cap, int64_t depth, int64_t width, int64_t experts
                     const int32_t* offsets, bool plan = true) {
   if (r_cap < 0 || depth < 1 || width < 1 || experts < 1 || experts > 1024) return EP_ERR_SHAPE;
   if (plan && (!counts != !offsets || (!counts && experts != 1))) return EP_ERR_SHAPE;
-  // a tile's rows are addressed by 32 bits of bytes, the grid by 31 bits of tiles
+  // a tile's rows are addressed by 32 bits of bytes
   if (r_cap >= ((int64_t)1 << 25) || depth > (1 << 20) || width > (1 << 20)) return EP_ERR_RANGE;
   return EP_OK;
 }
@@ -540,7 +540,7 @@ int32_t product_tiles(const uint16_t* rows, int64_t r_cap, int64_t K, const uint
                 const int32_t* counts, const int32_t* offsets, int64_t entries, uint16_t* out, hipStream_t s) {
   const Groups gr{counts, offsets, (int)E, (int)r_cap};
   const int64_t blocks = span_blocks(r_cap, E, !counts, entries, BM, (N + BN - 1) / BN);
-  if (blocks >= kSizeLimit) return EP_ERR_RANGE;
+  if (!grid_fits(blocks, 64 * WM * WN * SHARES)) return EP_ERR_RANGE;
   const size_t lds = Product<BM, BN, WM, WN, false, QT, SETS, SHARES>::kLds;
   hipLaunchKernelGGL((k_bf16_grouped_gemm<BM, BN, WM, WN, SETS, SHARES, QT>), dim3((unsigned)blocks), dim3(64 * WM * WN * SHARES), lds, s, rows, K,
                      weight, N, gr, out);
@@ -623,7 +623,7 @@ int32_t wgrad_tiles(const uint16_t* dout, const uint16_t* rows, int64_t width, i
                     OUT* out, hipStream_t s) {
   const int64_t per = ((width + BM - 1) / BM) * ((hidden + BN - 1) / BN), groups = (int64_t)parts * gr.experts;
   const int64_t blocks = per <= kWholeOnXcd<BM> ? (groups + 7) / 8 * 8 * per : groups * ((per + 7) / 8 * 8);
-  if (blocks >= kSizeLimit) return EP_ERR_RANGE;
+  if (!grid_fits(blocks, 64 * WM * WN * SHARES)) return EP_ERR_RANGE;
   const size_t lds = Product<BM, BN, WM, WN, true, true, SETS, SHARES>::kLds;
   hipLaunchKernelGGL((k_bf16_grouped_wgrad<BM, BN, WM, WN, SETS, SHARES, OUT>), dim3((unsigned)blocks), dim3(64 * WM * WN * SHARES), lds, s, dout,
                      width, rows, hidden, gr, parts, out);

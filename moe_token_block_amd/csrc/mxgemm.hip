@@ -442,7 +442,7 @@ int32_t mx_tiles(const uint8_t* data, const uint8_t* scales, int64_t r_cap, int6
                    int64_t entries, uint16_t* out, hipStream_t s) {
   const Groups gr{counts, offsets, (int)E, (int)r_cap};
   const int64_t blocks = span_blocks(r_cap, E, !counts, entries, BM, (N + BN - 1) / BN);
-  if (blocks >= kSizeLimit) return EP_ERR_RANGE;
+  if (!grid_fits(blocks, 64 * WM * WN * SHARES)) return EP_ERR_RANGE;
   const size_t lds = MxProduct<BM, BN, WM, WN, SHARES, A8>::kLds;
   hipLaunchKernelGGL((k_mxfp4_grouped_gemm<BM, BN, WM, WN, SHARES, A8>), dim3((unsigned)blocks), dim3(64 * WM * WN * SHARES), lds, s, data,
                      scales, (int)K, wcodes, wscales, N, gr, out);

@@ -95,6 +95,17 @@ def test_validation_before_launch(lib):
     assert d(P, P, P, P, N, 40, 64, P, P, ctypes.c_void_p(0x1004), ws, N) == -7
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="passes fake pointers: only where no GPU exists")
+def test_grids_that_do_not_fit(lib):
+    """Sizes within every other limit whose output tiles would need 2^32 threads."""
+    P, N, wide, e = ctypes.c_void_p(0x1000), None, 1 << 20, 1024
+    assert lib.ep_bf16_grouped_dgrad(P, 32, 1, P, e, wide, P, P, 32, P, N) == -8
+    assert lib.ep_bf16_grouped_gemm(P, 192 * e, 32, P, e, wide, P, P, 192 * e, P, N) == -8
+    assert lib.ep_bf16_grouped_wgrad(P, P, 32, 257, wide, e, P, P, 32, P, 0, N, 0, N) == -8
+    for fmt in (0, 1):
+        assert lib.ep_mxfp4_grouped_gemm(P, P, fmt, 192 * e, 32, P, P, e, wide, P, P, 192 * e, P, N) == -8
+
+
 def test_binding_refuses_cpu_tensors(lib):
     import moe_token_block_amd as m
     bf = torch.zeros((2, 64), dtype=torch.bfloat16)
