@@ -624,7 +624,8 @@ int32_t ep_bf16_grouped_wgrad(const uint16_t* dout, const uint16_t* rows, int64_
  * [rows, hidden/2] and scales [rows, hidden/32].  A block with an infinity or a NaN
  * gets scale byte 255: all of it reads back as NaN.  ep_mxfp4_unpack: the values as
  * BF16, rounded once (exact but at its ends).
- *   Requires hidden a positive multiple of 32, at most 2^24; rows * hidden < 2^40. */
+ *   Requires hidden a positive multiple of 32, at most 2^24, and rows * hidden < 2^34
+ *   (EP_ERR_RANGE). */
 int32_t ep_mxfp4_pack(const uint16_t* x, int64_t rows, int64_t hidden, uint8_t* codes, uint8_t* scales, void* stream);
 int32_t ep_mxfp4_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t hidden, uint16_t* out,
                         void* stream);
@@ -657,8 +658,8 @@ int32_t ep_mxfp4_grouped_gemm(const uint8_t* data, const uint8_t* scales, int32_
  *   block of 32 with an infinity or a NaN gets scale byte 255
  *   x, residual, h [rows, hidden] and weight [hidden] BF16, data [rows, hidden],
  *   scales [rows, hidden/32], rstd [rows] FP32.  Requires hidden a positive multiple
- *   of 32, at most 16384; rows < 2^30; eps from 2^-100 to 1e30; FP32 has to hold the sum of a row's
- *   squares.  h may be x or residual (the same address).
+ *   of 32, at most 16384; rows < 2^23 (EP_ERR_RANGE); eps from 2^-100 to 1e30; FP32
+ *   has to hold the sum of a row's squares.  h may be x or residual (the same address).
  * drmsnorm: with g = weight * dy,
  *   dx = rstd * (g - h * rstd^2 * mean(g * h)) + dh, rounded once to BF16 (dh NULL:
  *   nothing added): the gradient of x and of residual, dh being h's own from the

@@ -64,8 +64,8 @@ using namespace mtb;
 namespace {
 int32_t check(int64_t rows, int64_t hidden) {
   if (rows < 0 || hidden <= 0 || hidden % 32 != 0) return EP_ERR_SHAPE;
-  // one lane per 8 values, fewer than 2^31 workgroups of 256
-  if (hidden > (1 << 24) || rows > (((int64_t)1 << 40) - 1) / hidden) return EP_ERR_RANGE;
+  // one lane per 8 values, fewer than 2^31 lanes: a grid has less than 2^32
+  if (hidden > (1 << 24) || rows > (((int64_t)1 << 34) - 1) / hidden) return EP_ERR_RANGE;
   return EP_OK;
 }
 }  // namespace

@@ -243,7 +243,7 @@ namespace {
 
 int32_t check_sizes(int64_t rows, int64_t hidden) {
   if (rows < 0 || hidden < 32 || hidden % 32 != 0 || hidden > 16384) return EP_ERR_SHAPE;
-  if (rows >= ((int64_t)1 << 30)) return EP_ERR_RANGE;
+  if (rows >= ((int64_t)1 << 23)) return EP_ERR_RANGE;  // a row has up to 512 of the grid's 2^32 threads
   return EP_OK;
 }
 

@@ -106,6 +106,15 @@ def test_grids_that_do_not_fit(lib):
         assert lib.ep_mxfp4_grouped_gemm(P, P, fmt, 192 * e, 32, P, P, e, wide, P, P, 192 * e, P, N) == -8
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="passes fake pointers: only where no GPU exists")
+def test_rows_past_one_grid(lib):
+    P, N = ctypes.c_void_p(0x1000), None
+    assert lib.ep_mxfp4_pack(P, 1 << 29, 32, P, P, N) == -8
+    assert lib.ep_mxfp4_unpack(P, P, 1 << 29, 32, P, N) == -8
+    assert lib.rmsnorm_mxfp8(P, P, P, 1 << 23, 16384, 1e-6, P, P, P, P, N) == -8
+    assert lib.drmsnorm(P, P, P, P, N, 1 << 23, 64, P, P, P, 1 << 40, N) == -8
+
+
 def test_binding_refuses_cpu_tensors(lib):
     import moe_token_block_amd as m
     bf = torch.zeros((2, 64), dtype=torch.bfloat16)
