@@ -12,7 +12,7 @@
 //
 // Measured: 131072 MXFP4 rows of 32 experts, 7168 x 4096, 2.24 to 2.41 ms, 3190 to 3430
 // TFLOP/s (the unit's own rate is 10 PFLOP/s, 5 for MXFP8 rows); 32768 MXFP8 rows of 8
-// experts, 4096 x 4096, 550 us, 2000 TFLOP/s.  A step has the bytes of a BF16 step of a
+// experts, 4096 x 4096, 520 to 530 us, 2090 TFLOP/s.  A step has the bytes of a BF16 step of a
 // quarter of its terms, and the same parts bound it: barriers, LDS reads behind them, a
 // tile's first loads and its stores, 28 steps in 7168 values instead of 112.  A second
 // set of loads under way did not help (the small tiles then spill).
@@ -128,8 +128,7 @@ struct MxProduct {
   static constexpr int kOut = WM * WN * MT * 2048, kAll = 2 * SHARES * kBuf, kLds = kAll > kOut ? kAll : kOut;
   f32x4 acc[MT][NT];
 
-  // A step's products in kParts parts, `between(part)` called before each: the lanes'
-  // scales and operands come from LDS as they are needed.
+  // A step's products in kParts parts, `between(part)` called before each.
   static constexpr int kParts = A8 ? MT : 8;
   template <typename F>
   __device__ __forceinline__ void compute(const char* a_lds, const char* w_lds, int wm, int wn, F&& between) {
@@ -146,29 +145,39 @@ struct MxProduct {
       const char* at = a_lds + BM * 128 + (16 * (wm * MT + j) + r) * SB;
       sa[j] = A8 ? (int)*reinterpret_cast<const uint8_t*>(at + g) : (int)*reinterpret_cast<const uint16_t*>(at + 2 * g);
     }
-    u32x4 w[NT];
-    static_for<0, kParts>([&](auto part) {
-      constexpr int c = decltype(part)::value;
-      if constexpr (A8) {
-        // lane group g: weights 32 g .. + 31, row values 16 g .. + 15 and 64 + 16 g .. + 15,
-        // the scale of values 32 g .. + 31, as the instruction has them
-        if constexpr (c == 0) {
+    if constexpr (A8) {
+      // lane group g: weights 32 g .. + 31, row values 16 g .. + 15 and 64 + 16 g .. + 15,
+      // the scale of values 32 g .. + 31, as the instruction has them
+      u32x4 w[NT], a[2][2];
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
-            w[i] = *reinterpret_cast<const u32x4*>(w_lds + chunk_at<kRowW>(16 * (wn * NT + i) + r, g));
-        }
+      for (int i = 0; i < NT; ++i)
+        w[i] = *reinterpret_cast<const u32x4*>(w_lds + chunk_at<kRowW>(16 * (wn * NT + i) + r, g));
+      auto read = [&](auto part) {
+        constexpr int c = decltype(part)::value;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          a[c & 1][h] = *reinterpret_cast<const u32x4*>(a_lds + chunk_at<128>(16 * (wm * MT + c) + r, 4 * h + g));
+      };
+      read(std::integral_constant<int, 0>{});
+      static_for<0, kParts>([&](auto part) {
+        constexpr int c = decltype(part)::value;
+        // ahead of the stores in `between`, which no LDS read passes (32768 rows of 8 experts,
+        // 4096 x 4096: 521 us, read behind them 543)
+        if constexpr (c + 1 < kParts) read(std::integral_constant<int, c + 1>{});
         between(part);
-        const int row = 16 * (wm * MT + c) + r;
-        const i32x8 a = wide(*reinterpret_cast<const u32x4*>(a_lds + chunk_at<128>(row, g)),
-                             *reinterpret_cast<const u32x4*>(a_lds + chunk_at<128>(row, 4 + g)));
 #pragma unroll
         for (int i = 0; i < NT; ++i)
-          acc[c][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(w[i], none), a, acc[c][i], kE2M1, kE4M3, 0,
-                                                                       sw[i], 0, sa[c]);
-      } else {
-        // lane group g: values 32 g .. + 31 of the step's first half, then of its second
-        // (neighbouring chunks: groups that took every other one would meet in LDS's banks)
-        constexpr int S = c / 4, J = MT / 4;
+          acc[c][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(w[i], none), wide(a[c & 1][0], a[c & 1][1]),
+                                                                       acc[c][i], kE2M1, kE4M3, 0, sw[i], 0, sa[c]);
+      });
+    } else {
+      // lane group g: values 32 g .. + 31 of the step's first half, then of its second
+      // (neighbouring chunks: groups that took every other one would meet in LDS's banks).
+      // Rows' operands are read as needed: a part ahead took 41 us instead of 30 (1024 rows
+      // of 8 experts, 4096 x 4096, small tiles) and 2340 instead of 2310 (large ones).
+      u32x4 w[NT];
+      static_for<0, kParts>([&](auto part) {
+        constexpr int c = decltype(part)::value, S = c / 4, J = MT / 4;
         if constexpr (c % 4 == 0) {
 #pragma unroll
           for (int i = 0; i < NT; ++i)
@@ -183,8 +192,8 @@ struct MxProduct {
             acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(w[i], none), wide(a, none), acc[j][i], kE2M1,
                                                                          kE2M1, S, sw[i], S, sa[j]);
         }
-      }
-    });
+      });
+    }
   }
 
   __device__ __forceinline__ void run(char* all_lds, const uint8_t* a, const uint8_t* as, int a_n, const uint8_t* w,
