@@ -2,17 +2,17 @@
 //   out[g, n] = sum over blocks b of 32 of 2^(sa[g, b] - 127) 2^(sw[n, b] - 127)
 //               sum_i a[g, 32 b + i] w[n, 32 b + i]
 // on v_mfma_scale_f32_16x16x128_f8f6f4, which takes the codes and the blocks'
-// scale bytes as they are stored: nothing is decoded.  Sums are FP32.  For MXFP4
-// rows every product is exact and so is the sum of a block.  For MXFP8 rows the
-// instruction adds eight neighbouring products at a time, each cut at 2^-13 of the
-// largest of the eight (measured: 16 + 2^-9 is kept, 32 + 2^-9 is not; across the
-// eights the sum has FP32's width), at most 2^-10 of the sum of the terms'
-// magnitudes and a quarter of the result's own BF16 rounding where terms do not
-// cancel.  Decoding to BF16 instead would be exact, at half of the rate.
+// scale bytes as they are stored.  Sums are FP32 and every product is exact in them.
+// The instruction adds eight neighbouring products at a time, each cut 13 bits below the
+// largest one's exponent (of the factors' own: mantissas do not count).  E2M1 products
+// span 2^7 and lose nothing; E4M3 times E2M1 span 2^21, so MXFP8 rows are multiplied as
+// the sum of two parts of eight exponents each (split_e4m3), which lose nothing either: at
+// twice the instructions, the BF16 rate, and as exact as decoding to BF16, without the
+// decoded operands' LDS and registers.
 //
 // Measured: 131072 MXFP4 rows of 32 experts, 7168 x 4096, 2.24 to 2.41 ms, 3190 to 3430
-// TFLOP/s (the unit's own rate is 10 PFLOP/s, 5 for MXFP8 rows); 32768 MXFP8 rows of 8
-// experts, 4096 x 4096, 520 to 530 us, 2090 TFLOP/s.  A step has the bytes of a BF16 step of a
+// TFLOP/s (the unit's own rate is 10 PFLOP/s, 2.5 for MXFP8 rows); 32768 MXFP8 rows of 8
+// experts, 4096 x 4096, 0.88 ms, 1250 TFLOP/s.  A step has the bytes of a BF16 step of a
 // quarter of its terms, and the same parts bound it: barriers, LDS reads behind them, a
 // tile's first loads and its stores, 28 steps in 7168 values instead of 112.  A second
 // set of loads under way did not help (the small tiles then spill).
@@ -26,6 +26,19 @@ constexpr int kE2M1 = 4, kE4M3 = 0;  // the instruction's operand formats
 
 __device__ __forceinline__ i32x8 wide(u32x4 lo, u32x4 hi) {
   return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+}
+
+// E4M3 bytes as the sum of those of magnitude 2 and more (exponents 1 to 8; the NaN) and
+// the others (-6 to 0, the subnormals among them): bit 6 of a byte tells.  Zeros are in
+// the places of values of the other part.
+__device__ __forceinline__ void split_e4m3(u32x4 v, u32x4& high, u32x4& low) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // selectors 8 to 11 repeat bits 15 and 31 of the second and of the first source over a byte
+    const uint32_t m = __builtin_amdgcn_perm(v[i] << 1, v[i] << 9, 0x0B090A08u);
+    high[i] = v[i] & m;
+    low[i] = v[i] & ~m;
+  }
 }
 
 // Where chunk c (16 bytes) of a tile row lies in LDS, so that eight lanes reading
@@ -161,14 +174,20 @@ struct MxProduct {
       read(std::integral_constant<int, 0>{});
       static_for<0, kParts>([&](auto part) {
         constexpr int c = decltype(part)::value;
-        // ahead of the stores in `between`, which no LDS read passes (32768 rows of 8 experts,
-        // 4096 x 4096: 521 us, read behind them 543)
+        // ahead of the stores in `between`, which no LDS read passes
         if constexpr (c + 1 < kParts) read(std::integral_constant<int, c + 1>{});
         between(part);
+        u32x4 high[2], low[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) split_e4m3(a[c & 1][h], high[h], low[h]);
 #pragma unroll
         for (int i = 0; i < NT; ++i)
-          acc[c][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(w[i], none), wide(a[c & 1][0], a[c & 1][1]),
-                                                                       acc[c][i], kE2M1, kE4M3, 0, sw[i], 0, sa[c]);
+          acc[c][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(w[i], none), wide(low[0], low[1]), acc[c][i],
+                                                                       kE2M1, kE4M3, 0, sw[i], 0, sa[c]);
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          acc[c][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(w[i], none), wide(high[0], high[1]), acc[c][i],
+                                                                       kE2M1, kE4M3, 0, sw[i], 0, sa[c]);
       });
     } else {
       // lane group g: values 32 g .. + 31 of the step's first half, then of its second
@@ -309,13 +328,22 @@ __global__ __launch_bounds__(64 * WM * WN * SHARES) void k_mxfp4_grouped_gemm(co
              wscales + col * (K / 32), (int)min((int64_t)BN, N - n0), K);
   else
     prod.run(lds, data, scales, 1, wcodes, wscales, 1, 0);
-  static_assert(P::NT == 4, "a wave stores 64 columns");
+  static_assert(P::NT % 4 == 0, "a wave stores 64 columns at a time");
   if (s.extent > BM)
     clear_rows(out + row * N + n0, N, BM, s.extent, (int)min((int64_t)BN, N - n0));
   if (wave >= WM * WN) return;
-  const int m = wm * P::MT * 16, n = n0 + wn * 64;
-  store_block64<P::MT>(prod.acc, lds + wave * P::MT * 2048, out + (row + m) * N + n, N, s.used - m, s.extent - m,
-                       (int)min((int64_t)64, N - n));
+  const int m = wm * P::MT * 16;
+  static_for<0, P::NT / 4>([&](auto block) {
+    constexpr int b = decltype(block)::value;
+    f32x4 acc[P::MT][4];
+#pragma unroll
+    for (int j = 0; j < P::MT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j][i] = prod.acc[j][4 * b + i];
+    const int n = n0 + (wn * P::NT / 4 + b) * 64;
+    store_block64<P::MT>(acc, lds + wave * P::MT * 2048, out + (row + m) * N + n, N, s.used - m, s.extent - m,
+                         (int)min((int64_t)64, N - n));
+  });
 }
 
 // For experts with few rows, where the time is that of reading the weights.  A
@@ -325,7 +353,7 @@ __global__ __launch_bounds__(64 * WM * WN * SHARES) void k_mxfp4_grouped_gemm(co
 // registers, four lanes on 64 contiguous bytes, and are brought into the instruction's
 // order within lane quads; a step's loads are in flight while the step before is
 // multiplied.  One token, 2 of 8 experts of 4096 x 2048: 4.5 us for 9.9 MB; 128 rows of 32
-// experts of 4096 x 7168: 94 us for 500 MB (5.3 TB/s), MXFP8 rows 131.
+// experts of 4096 x 7168: 94 us for 500 MB (5.3 TB/s), MXFP8 rows 143.
 template <int RT, int NT, bool A8>
 __global__ __launch_bounds__(NT == 1 ? 512 : 256) void k_mxfp4_grouped_few(
     const uint8_t* __restrict__ data, const uint8_t* __restrict__ scales, int K, const uint8_t* __restrict__ wcodes,
@@ -419,12 +447,23 @@ __global__ __launch_bounds__(NT == 1 ? 512 : 256) void k_mxfp4_grouped_few(
       static_for<0, 4>([&](auto block) {
         constexpr int j = decltype(block)::value;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t) {
+          i32x8 x = wide(d.x[t][0][j], none);
+          if constexpr (A8) {
+            u32x4 high[2], low[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) split_e4m3(d.x[t][h][j], high[h], low[h]);
+            x = wide(high[0], high[1]);
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+              acc[t][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(d.w[i][j], none), wide(low[0], low[1]), acc[t][i],
+                                                                           kE2M1, kE4M3, j, (int)d.sw[i], j, (int)d.sx[t]);
+          }
 #pragma unroll
           for (int i = 0; i < RT; ++i)
-            acc[t][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                wide(d.w[i][j], none), wide(d.x[t][0][j], A8 ? d.x[t][H - 1][j] : none), acc[t][i], kE2M1,
-                A8 ? kE4M3 : kE2M1, j, (int)d.sw[i], j, (int)d.sx[t]);
+            acc[t][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(d.w[i][j], none), x, acc[t][i], kE2M1,
+                                                                         A8 ? kE4M3 : kE2M1, j, (int)d.sw[i], j, (int)d.sx[t]);
+        }
       });
     };
     Step s0, s1;
@@ -478,8 +517,8 @@ int32_t mx_product(const uint8_t* data, const uint8_t* scales, int64_t r_cap, in
   const int64_t groups = few_groups(r_cap, E, !counts);
   // Up to 16 rows an expert (on average) by the kernel that streams the weights, MXFP4
   // rows 32 weight rows at a time, MXFP8 rows, which take twice the registers, 16: 32
-  // experts of 4096 x 7168, 8 rows each, 99 us (tiles 137) and 141 (192); 16 rows 132
-  // (140) and 193 (197); 32 rows 199 (148) and 297 (207).
+  // experts of 4096 x 7168, 8 rows each, 99 us (tiles 137) and 153 (231); 16 rows 132
+  // (140) and 223 (234); 32 rows of MXFP4 199 (148).
   // With more rows, too, where a long sum would be left to few tiles: a workgroup for
   // each 16 rows.
   constexpr int RT = A8 ? 1 : 2;
@@ -488,15 +527,24 @@ int32_t mx_product(const uint8_t* data, const uint8_t* scales, int64_t r_cap, in
   if ((mean <= 16 || thin) && groups <= 65535)
     return mx_few<RT, 1, A8>(data, scales, r_cap, K, wcodes, wscales, E, N, counts, offsets,
                              dim3(1, (unsigned)groups, (unsigned)chunks), out, 4, s);
-  // Large tiles from 192 rows an expert on where they reach about half of the CUs: 8
-  // experts of 4096 x 4096, 259 rows each (256 tiles), 40 us, by small ones 52; 128 rows
-  // each 35 and 31; 4 experts of 1024 x 2048, 512 rows each (32 tiles), 22 and 13.
-  if (mean >= 192 && E * ((mean + 255) / 256) * ((N + 255) / 256) >= 112)
+  // Large tiles from 192 rows an expert on.  MXFP4 rows: where they reach about half of the
+  // CUs: 8 experts of 4096 x 4096, 259 rows each (256 tiles), 40 us, by small ones 52; 128
+  // rows each 35 and 31; 4 experts of 1024 x 2048, 512 rows each (32 tiles), 22 and 13.
+  // MXFP8 rows, whose waves split their rows' operands once in a small tile and four times
+  // over in a large one: from six tiles a CU on: 8 experts of 4096 x 4096, 259 rows each 96
+  // and 88, 2048 rows each (1024 tiles) 477 and 455, 4096 (2048 tiles) 880 and 887; 32 of
+  // 4096 x 7168, 1024 rows each (2048 tiles), 1573 and 1638.
+  if (mean >= 192 && E * ((mean + 255) / 256) * ((N + 255) / 256) >= (A8 ? 1536 : 112))
     return mx_tiles<256, 256, 2, 4, 1, A8>(data, scales, r_cap, K, wcodes, wscales, E, N, counts, offsets, entries, out, s);
-  // Small ones: where they are fewer than the CUs two groups of waves share the sum.
+  // Small ones: where they are fewer than the CUs two groups of waves share the sum (MXFP8
+  // rows, 4 experts of 1024 x 2048, 512 rows each: 18.0 us, by one group 22.1; 8 of 4096 x
+  // 4096, 128 rows each (256 tiles): 61.7 and 54.2).  MXFP8 rows' waves lie one below the
+  // other, each with all of the tile's columns, so that no two split the same rows (8 of 4096
+  // x 4096, 128 rows each: 54 us, two by two 61).
+  constexpr int WM = A8 ? 4 : 2, WN = A8 ? 1 : 2;
   if (E * ((mean + 127) / 128) * ((N + 127) / 128) <= 192)
-    return mx_tiles<128, 128, 2, 2, 2, A8>(data, scales, r_cap, K, wcodes, wscales, E, N, counts, offsets, entries, out, s);
-  return mx_tiles<128, 128, 2, 2, 1, A8>(data, scales, r_cap, K, wcodes, wscales, E, N, counts, offsets, entries, out, s);
+    return mx_tiles<128, 128, WM, WN, 2, A8>(data, scales, r_cap, K, wcodes, wscales, E, N, counts, offsets, entries, out, s);
+  return mx_tiles<128, 128, WM, WN, 1, A8>(data, scales, r_cap, K, wcodes, wscales, E, N, counts, offsets, entries, out, s);
 }
 }  // namespace
 
