@@ -596,8 +596,9 @@ int32_t dswiglu_mxfp8_checkpoint(const uint8_t* data, const uint8_t* scales, con
  *   ep_bf16_grouped_dgrad: drows[g, k] = sum_n dout[g, n] weight[e, n, k]
  *   ep_bf16_grouped_wgrad: dweight[e, n, k] = sum_g dout[g, n] rows[g, k]
  * rows and drows [r_cap, hidden], dout and out [r_cap, width], weight [E, width,
- * hidden] BF16; dweight [E, width, hidden] BF16 or (f32 != 0) FP32.  Sums are FP32
- * in an order fixed by the sizes and the plan, rounded once.  Grouped rows that hold
+ * hidden] BF16; dweight [E, width, hidden] BF16 or (f32 != 0) FP32.  Products are
+ * exact and sums FP32 in an order fixed by the sizes and the plan, rounded once; a BF16
+ * number below the normal range counts in the sum's rounding as 2^-126.  Grouped rows that hold
  * no entry are not used; the first two write every row below r_cap that
  * the plan's spans cover or that lies behind them, zeros where there is no entry,
  * and the third writes every expert's weights, zeros for one without entries.
