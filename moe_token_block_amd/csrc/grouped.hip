@@ -372,7 +372,6 @@ __global__ __launch_bounds__(NT == 1 ? 512 : 256) void k_bf16_grouped_few(const 
 // sum's terms: a wave's 64 of them by 64 columns go through LDS of its own, whose
 // transposing read makes the instruction's operand.  One token, 2 of 8 experts of 4096 x
 // 2048: 16.5 us for 34 MB; 128 rows, 8 experts of 4096 x 4096: 63 us for 270 MB.
-template <int NT>
 __global__ __launch_bounds__(512) void k_bf16_grouped_few_across(const uint16_t* __restrict__ dout, int64_t N,
                                                                  const uint16_t* __restrict__ weight, int64_t K,
                                                                  Groups gr, uint16_t* __restrict__ drows) {
@@ -385,6 +384,7 @@ __global__ __launch_bounds__(512) void k_bf16_grouped_few_across(const uint16_t*
   if (blockIdx.z == 0) clear_rows(drows + (int64_t)lo * K + k0, K, cnt, hi - lo, cols);
   const int r = lane & 15, g = lane >> 4;
   char* own = lds + wave * 8192;
+  constexpr int NT = 2;  // 32 rows at a time
   const int steps = (int)((N + 63) / 64);
   for (int c0 = 16 * NT * (int)blockIdx.z; c0 < cnt; c0 += 16 * NT * (int)gridDim.z) {
     const int used = min(cnt - c0, 16 * NT);
@@ -450,11 +450,11 @@ constexpr int kWholeOnXcd = BM == 256 ? 32 : 64;
 // equal runs; FP32, share i at out + i * E * N * K): P dout's columns, Q the rows'.  Short
 // sums are bound by a tile's fixed costs: 222 rows an expert, 32 of 2040 x 2440, 200 us
 // for 380 MB.
-template <int BM, int BN, int WM, int WN, int SETS, int SHARES, typename OUT>
-__global__ __launch_bounds__(64 * WM * WN * SHARES) void k_bf16_grouped_wgrad(const uint16_t* __restrict__ dout, int64_t N,
+template <int BM, int BN, int WM, int WN, typename OUT>
+__global__ __launch_bounds__(64 * WM * WN) void k_bf16_grouped_wgrad(const uint16_t* __restrict__ dout, int64_t N,
                                                                      const uint16_t* __restrict__ rows, int64_t K,
                                                                      Groups gr, int parts, OUT* __restrict__ out) {
-  typedef Product<BM, BN, WM, WN, true, true, SETS, SHARES> P;
+  typedef Product<BM, BN, WM, WN, true, true, 1, 1> P;
   extern __shared__ char lds[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave / WN, wn = wave % WN;
   const int tm = (int)((N + BM - 1) / BM), tn = (int)((K + BN - 1) / BN);
@@ -487,7 +487,6 @@ __global__ __launch_bounds__(64 * WM * WN * SHARES) void k_bf16_grouped_wgrad(co
   P prod;
   prod.run(lds, dout + (int64_t)lo * N + m0, N, (int)min((int64_t)BM, N - m0), rows + (int64_t)lo * K + n0, K,
            (int)min((int64_t)BN, K - n0), cnt);
-  if (wave >= WM * WN) return;
   const int m = m0 + wm * P::MT * 16, n = n0 + wn * 64;
   OUT* o = out + (((int64_t)part * gr.experts + e) * N + m) * K + n;
   const int rest = (int)(N - m), cols = (int)min((int64_t)64, K - n);
@@ -547,7 +546,6 @@ int32_t product_tiles(const uint16_t* rows, int64_t r_cap, int64_t K, const uint
   return launch_status();
 }
 
-
 template <int RT, int NT>
 int32_t product_few(const uint16_t* rows, int64_t r_cap, int64_t K, const uint16_t* weight, int64_t E, int64_t N,
                     const int32_t* counts, const int32_t* offsets, dim3 grid, uint16_t* out, int waves, hipStream_t s) {
@@ -564,7 +562,7 @@ int32_t product_few_across(const uint16_t* dout, int64_t r_cap, int64_t N, const
   const Groups gr{counts, offsets, (int)E, (int)r_cap};
   const int W = N > 64 * 7 ? 8 : (int)((N + 63) / 64);  // no wave without a step
   grid.x = (unsigned)((K + 63) / 64);
-  hipLaunchKernelGGL(k_bf16_grouped_few_across<2>, grid, dim3(64 * W), (size_t)W * 8192, s, dout, N, weight, K, gr, drows);
+  hipLaunchKernelGGL(k_bf16_grouped_few_across, grid, dim3(64 * W), (size_t)W * 8192, s, dout, N, weight, K, gr, drows);
   return launch_status();
 }
 
@@ -618,14 +616,14 @@ int32_t product(const uint16_t* rows, int64_t r_cap, int64_t K, const uint16_t* 
   return product_tiles<128, 128, 2, 2, QT ? 1 : 2, 1, QT>(rows, r_cap, K, weight, E, N, counts, offsets, entries, out, s);
 }
 
-template <int BM, int BN, int WM, int WN, int SETS, int SHARES, typename OUT>
+template <int BM, int BN, int WM, int WN, typename OUT>
 int32_t wgrad_tiles(const uint16_t* dout, const uint16_t* rows, int64_t width, int64_t hidden, const Groups& gr, int parts,
                     OUT* out, hipStream_t s) {
   const int64_t per = ((width + BM - 1) / BM) * ((hidden + BN - 1) / BN), groups = (int64_t)parts * gr.experts;
   const int64_t blocks = per <= kWholeOnXcd<BM> ? (groups + 7) / 8 * 8 * per : groups * ((per + 7) / 8 * 8);
-  if (!grid_fits(blocks, 64 * WM * WN * SHARES)) return EP_ERR_RANGE;
-  const size_t lds = Product<BM, BN, WM, WN, true, true, SETS, SHARES>::kLds;
-  hipLaunchKernelGGL((k_bf16_grouped_wgrad<BM, BN, WM, WN, SETS, SHARES, OUT>), dim3((unsigned)blocks), dim3(64 * WM * WN * SHARES), lds, s, dout,
+  if (!grid_fits(blocks, 64 * WM * WN)) return EP_ERR_RANGE;
+  const size_t lds = Product<BM, BN, WM, WN, true, true, 1, 1>::kLds;
+  hipLaunchKernelGGL((k_bf16_grouped_wgrad<BM, BN, WM, WN, OUT>), dim3((unsigned)blocks), dim3(64 * WM * WN), lds, s, dout,
                      width, rows, hidden, gr, parts, out);
   return launch_status();
 }
@@ -647,7 +645,7 @@ int32_t wgrad(const uint16_t* dout, const uint16_t* rows, int64_t width, int64_t
               OUT* out, float* workspace, hipStream_t s) {
   const int parts = wgrad_parts(width, hidden, gr.experts, entries);
   if (parts > 1) {
-    const int32_t st = wgrad_tiles<128, 128, 2, 2, 1, 1>(dout, rows, width, hidden, gr, parts, workspace, s);
+    const int32_t st = wgrad_tiles<128, 128, 2, 2>(dout, rows, width, hidden, gr, parts, workspace, s);
     if (st != EP_OK) return st;
     const int64_t n = gr.experts * width * hidden;
     hipLaunchKernelGGL(k_wgrad_join<OUT>, dim3((unsigned)((n + 1023) / 1024)), dim3(256), 0, s, workspace, parts, n, out);
@@ -657,8 +655,8 @@ int32_t wgrad(const uint16_t* dout, const uint16_t* rows, int64_t width, int64_t
   // 512 rows each, 175 us, by small ones 234; 32 of 512 x 512 (128), 4096 rows, 105 and 97;
   // 4 of 1024 x 2048 (128), 2048 rows, 55 (57 in two shares) and 45.
   if (gr.experts * ((width + 255) / 256) * ((hidden + 255) / 256) >= 256)
-    return wgrad_tiles<256, 256, 2, 4, 1, 1>(dout, rows, width, hidden, gr, 1, out, s);
-  return wgrad_tiles<128, 128, 2, 2, 1, 1>(dout, rows, width, hidden, gr, 1, out, s);
+    return wgrad_tiles<256, 256, 2, 4>(dout, rows, width, hidden, gr, 1, out, s);
+  return wgrad_tiles<128, 128, 2, 2>(dout, rows, width, hidden, gr, 1, out, s);
 }
 
 }  // namespace

@@ -347,19 +347,19 @@ __global__ __launch_bounds__(64 * WM * WN * SHARES) void k_mxfp4_grouped_gemm(co
 }
 
 // For experts with few rows, where the time is that of reading the weights.  A
-// workgroup takes 16 RT weight rows of one expert and 16 NT of its rows at a time (the
+// workgroup takes 16 RT weight rows of one expert and 16 of its rows at a time (the
 // z-th of gridDim.z first, then every gridDim.z-th); its waves take the sum's steps of
 // 512 values in turn and join their sums through LDS.  Codes go from memory to
 // registers, four lanes on 64 contiguous bytes, and are brought into the instruction's
 // order within lane quads; a step's loads are in flight while the step before is
 // multiplied.  One token, 2 of 8 experts of 4096 x 2048: 4.5 us for 9.9 MB; 128 rows of 32
 // experts of 4096 x 7168: 94 us for 500 MB (5.3 TB/s), MXFP8 rows 143.
-template <int RT, int NT, bool A8>
-__global__ __launch_bounds__(NT == 1 ? 512 : 256) void k_mxfp4_grouped_few(
+template <int RT, bool A8>
+__global__ __launch_bounds__(256, 2) void k_mxfp4_grouped_few(
     const uint8_t* __restrict__ data, const uint8_t* __restrict__ scales, int K, const uint8_t* __restrict__ wcodes,
     const uint8_t* __restrict__ wscales, int64_t N, Groups gr, uint16_t* __restrict__ out) {
   extern __shared__ char lds[];
-  float* red = reinterpret_cast<float*>(lds);  // [waves][RT * NT][16 rows][16 columns]
+  float* red = reinterpret_cast<float*>(lds);  // [waves][RT][16 rows][16 columns]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), W = blockDim.x >> 6;
   const int n0 = (int)blockIdx.x * 16 * RT, cols = (int)min((int64_t)16 * RT, N - n0), e = blockIdx.y;
   int lo, hi, cnt;
@@ -386,8 +386,8 @@ __global__ __launch_bounds__(NT == 1 ? 512 : 256) void k_mxfp4_grouped_few(
   const int steps = (K + 511) / 512;
   constexpr int H = A8 ? 2 : 1;
   struct Step {
-    u32x4 w[RT][4], x[NT][H][4];
-    uint32_t sw[RT], sx[NT];
+    u32x4 w[RT][4], x[H][4];
+    uint32_t sw[RT], sx;
   };
   auto scale4 = [](const uint8_t* p, int n) {
     if (n >= 4) return ld_any<uint32_t>(p);
@@ -397,22 +397,17 @@ __global__ __launch_bounds__(NT == 1 ? 512 : 256) void k_mxfp4_grouped_few(
       if (b < n) v |= (uint32_t)p[b] << (8 * b);
     return v;
   };
-  for (int c0 = 16 * NT * (int)blockIdx.z; c0 < cnt; c0 += 16 * NT * (int)gridDim.z) {
-    const int used = min(cnt - c0, 16 * NT);
+  for (int c0 = 16 * (int)blockIdx.z; c0 < cnt; c0 += 16 * (int)gridDim.z) {
+    const int used = min(cnt - c0, 16);
     const uint8_t* x = data + (int64_t)(lo + c0) * xrow + 16 * xchunk;
     const uint8_t* xs = scales + (int64_t)(lo + c0) * srow + 4 * g;
-    uint32_t xoff[NT][4], xsoff[NT];
+    uint32_t xoff[4];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
+    for (int j = 0; j < 4; ++j) xoff[j] = (uint32_t)min(b4 + j, used - 1) * xrow;
+    const uint32_t xsoff = (uint32_t)min(r, used - 1) * srow;
+    f32x4 acc[1][RT];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) xoff[i][j] = (uint32_t)min(16 * i + b4 + j, used - 1) * xrow;
-      xsoff[i] = (uint32_t)min(16 * i + r, used - 1) * srow;
-    }
-    f32x4 acc[NT][RT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < RT; ++i) acc[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < RT; ++i) acc[0][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     auto load = [&](int s, Step& d) {
       const u32x4 none = {0u, 0u, 0u, 0u};
       const int left = K - 512 * s;  // values from the step's first on
@@ -423,47 +418,39 @@ __global__ __launch_bounds__(NT == 1 ? 512 : 256) void k_mxfp4_grouped_few(
         for (int i = 0; i < RT; ++i)
           d.w[i][j] = whole || 32 * wchunk < left ? ld_any<u32x4>(w + woff[i][j] + 256 * s) : none;
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int h = 0; h < H; ++h)
-            d.x[i][h][j] = whole || (A8 ? 16 * (xchunk + 16 * h) : 32 * xchunk) < left
-                               ? ld_any<u32x4>(x + xoff[i][j] + (A8 ? 512 : 256) * s + 256 * h)
-                               : none;
+        for (int h = 0; h < H; ++h)
+          d.x[h][j] = whole || (A8 ? 16 * (xchunk + 16 * h) : 32 * xchunk) < left
+                          ? ld_any<u32x4>(x + xoff[j] + (A8 ? 512 : 256) * s + 256 * h)
+                          : none;
       }
       const int blocks = whole ? 4 : left / 32 - 4 * g;
 #pragma unroll
       for (int i = 0; i < RT; ++i) d.sw[i] = scale4(ws + wsoff[i] + 16 * s, blocks);
-#pragma unroll
-      for (int i = 0; i < NT; ++i) d.sx[i] = scale4(xs + xsoff[i] + 16 * s, blocks);
+      d.sx = scale4(xs + xsoff + 16 * s, blocks);
     };
     auto multiply = [&](Step& d) {
       const u32x4 none = {0u, 0u, 0u, 0u};
 #pragma unroll
       for (int i = 0; i < RT; ++i) quad_transpose(d.w[i]);
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int h = 0; h < H; ++h) quad_transpose(d.x[i][h]);
+      for (int h = 0; h < H; ++h) quad_transpose(d.x[h]);
       static_for<0, 4>([&](auto block) {
         constexpr int j = decltype(block)::value;
+        i32x8 x = wide(d.x[0][j], none);
+        if constexpr (A8) {
+          u32x4 high[2], low[2];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          i32x8 x = wide(d.x[t][0][j], none);
-          if constexpr (A8) {
-            u32x4 high[2], low[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) split_e4m3(d.x[t][h][j], high[h], low[h]);
-            x = wide(high[0], high[1]);
-#pragma unroll
-            for (int i = 0; i < RT; ++i)
-              acc[t][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(d.w[i][j], none), wide(low[0], low[1]), acc[t][i],
-                                                                           kE2M1, kE4M3, j, (int)d.sw[i], j, (int)d.sx[t]);
-          }
+          for (int h = 0; h < 2; ++h) split_e4m3(d.x[h][j], high[h], low[h]);
+          x = wide(high[0], high[1]);
 #pragma unroll
           for (int i = 0; i < RT; ++i)
-            acc[t][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(d.w[i][j], none), x, acc[t][i], kE2M1,
-                                                                         A8 ? kE4M3 : kE2M1, j, (int)d.sw[i], j, (int)d.sx[t]);
+            acc[0][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(d.w[i][j], none), wide(low[0], low[1]), acc[0][i],
+                                                                         kE2M1, kE4M3, j, (int)d.sw[i], j, (int)d.sx);
         }
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+          acc[0][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(d.w[i][j], none), x, acc[0][i], kE2M1,
+                                                                       A8 ? kE4M3 : kE2M1, j, (int)d.sw[i], j, (int)d.sx);
       });
     };
     Step s0, s1;
@@ -475,7 +462,7 @@ __global__ __launch_bounds__(NT == 1 ? 512 : 256) void k_mxfp4_grouped_few(
       if (s + 2 * W < steps) load(s + 2 * W, s0);
       if (s + W < steps) multiply(s1);
     }
-    join_few<RT, NT>(acc, red, out + (int64_t)(lo + c0) * N + n0, N, used, cols);
+    join_few<RT, 1>(acc, red, out + (int64_t)(lo + c0) * N + n0, N, used, cols);
   }
 }
 
@@ -497,15 +484,15 @@ int32_t mx_tiles(const uint8_t* data, const uint8_t* scales, int64_t r_cap, int6
   return launch_status();
 }
 
-template <int RT, int NT, bool A8>
+template <int RT, bool A8>
 int32_t mx_few(const uint8_t* data, const uint8_t* scales, int64_t r_cap, int64_t K, const uint8_t* wcodes,
                const uint8_t* wscales, int64_t E, int64_t N, const int32_t* counts, const int32_t* offsets, dim3 grid,
-               uint16_t* out, int waves, hipStream_t s) {
+               uint16_t* out, hipStream_t s) {
   const Groups gr{counts, offsets, (int)E, (int)r_cap};
-  const int W = K > 512 * (waves - 1) ? waves : (int)((K + 511) / 512);  // no wave without a step
+  const int W = K > 512 * 3 ? 4 : (int)((K + 511) / 512);  // no wave without a step
   grid.x = (unsigned)((N + 16 * RT - 1) / (16 * RT));
-  hipLaunchKernelGGL((k_mxfp4_grouped_few<RT, NT, A8>), grid, dim3(64 * W), (size_t)W * RT * NT * 1024, s, data, scales,
-                     (int)K, wcodes, wscales, N, gr, out);
+  hipLaunchKernelGGL((k_mxfp4_grouped_few<RT, A8>), grid, dim3(64 * W), (size_t)W * RT * 1024, s, data, scales, (int)K,
+                     wcodes, wscales, N, gr, out);
   return launch_status();
 }
 
@@ -525,8 +512,8 @@ int32_t mx_product(const uint8_t* data, const uint8_t* scales, int64_t r_cap, in
   const int64_t chunks = mean > 16 ? (mean + 15) / 16 : 1;  // without entries, too: the rows are cleared
   const bool thin = K > 2048 && E * ((N + 16 * RT - 1) / (16 * RT)) * chunks <= 2048 && chunks <= 65535;
   if ((mean <= 16 || thin) && groups <= 65535)
-    return mx_few<RT, 1, A8>(data, scales, r_cap, K, wcodes, wscales, E, N, counts, offsets,
-                             dim3(1, (unsigned)groups, (unsigned)chunks), out, 4, s);
+    return mx_few<RT, A8>(data, scales, r_cap, K, wcodes, wscales, E, N, counts, offsets,
+                          dim3(1, (unsigned)groups, (unsigned)chunks), out, s);
   // Large tiles from 192 rows an expert on.  MXFP4 rows: where they reach about half of the
   // CUs: 8 experts of 4096 x 4096, 259 rows each (256 tiles), 40 us, by small ones 52; 128
   // rows each 35 and 31; 4 experts of 1024 x 2048, 512 rows each (32 tiles), 22 and 13.
