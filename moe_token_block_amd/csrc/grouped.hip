@@ -575,16 +575,19 @@ int32_t product(const uint16_t* rows, int64_t r_cap, int64_t K, const uint16_t* 
   // Few rows an expert (on average), or so few results that tiles would leave most CUs
   // idle: by blocks of 32 rows whose waves share out the sum.  8 experts of 4096 x 4096,
   // 4 rows each, 47 us (tiles 77); 32 of 4096 x 7168, 8 rows 312 (384), 16 rows 318 (390),
-  // 32 rows 460 (396); 256 rows times 512 x 1024, 4 experts (512 blocks), 10.5 (13.7), times
-  // 1024 x 2048 (2048 blocks) 42 (21.5).
+  // 32 rows 460 (396).  With more rows, up to 512 blocks: 4 experts of 512 x 1024, 256 rows
+  // each (512 blocks), 10.7 (13.0), 512 rows each (1024) 16.5 (13.3); 8 of 512 x 4096, 96 rows
+  // (384) 26 (34), 128 rows (512) 34.5 (33.8), 256 rows (1024) 67 (34); 4 of 2048 x 2048, 64
+  // rows (512) 18.2 (19.8), 128 rows (1024) 27 (20).
   const int64_t groups = few_groups(r_cap, E, !counts), chunks = (mean + 31) / 32;
   // Where the weights are read across, blocks are 64 columns wide, and many of them that
   // read each weight once are better off as tiles: 8 experts of 4096 x 4096, 16 rows, 63
-  // (82); 32 of 4096 x 7168, 8 rows, 417 (386); 256 rows times 512 x 1024, 4 experts (512
-  // blocks), 16.1 (10.5).
+  // (82); 32 of 4096 x 7168, 8 rows, 417 (386).  With more rows, up to 256 blocks: 4 experts
+  // of 1024 x 1024 (drows' columns first), 128 rows each, 13.2 (13.8); 2 of 1024 x 4096, 128
+  // rows (128 blocks), 18 (36); 8 of 2048 x 2048, 32 rows (256), 25 (21).
   const int64_t used = E < most ? E : most;  // experts with rows, at most
   const bool few = QT ? (mean <= 24 && used * ((N + 127) / 128) <= 1024) || E * ((N + 63) / 64) * chunks <= 256
-                      : mean <= 24 || E * ((N + 31) / 32) * chunks <= 1024;
+                      : mean <= 24 || E * ((N + 31) / 32) * chunks <= 512;
   if (few && groups <= 65535) {
     // workgroups beside each other for one expert's rows: as many as the mean asks for,
     // more (the loads may be uneven) where that leaves few
