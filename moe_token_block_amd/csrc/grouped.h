@@ -240,19 +240,22 @@ __device__ __forceinline__ void clear_rows(uint16_t* out, int64_t ld, int first,
     store8(out + (int64_t)(first + i / pieces) * ld + 8 * (i % pieces), u32x4{0u, 0u, 0u, 0u}, cols - 8 * (i % pieces));
 }
 
-// The kernels for few rows: blockIdx.y is an expert or, past the last, a stretch of
-// the rows behind it.
-inline int64_t few_groups(int64_t r_cap, int64_t experts, bool dense) {
-  return dense ? 1 : experts + r_cap / kTailRows + 1;
+// The kernels for few rows: blockIdx.y is an expert, whose rows gridDim.z workgroups
+// share, or, past the last, gridDim.z stretches of the rows behind it.
+inline int64_t few_groups(int64_t r_cap, int64_t experts, bool dense, int64_t z) {
+  return dense ? 1 : experts + (r_cap / kTailRows + z) / z;
 }
-// Its rows [lo, hi), the first cnt of which hold entries; false: none.
-__device__ __forceinline__ bool few_rows(const Groups& gr, int& lo, int& hi, int& cnt) {
+// Its rows [lo, hi), the first cnt of which hold entries, and the first row that this
+// workgroup clears; false: none.
+__device__ __forceinline__ bool few_rows(const Groups& gr, int& lo, int& hi, int& cnt, int& clear) {
   const int e = blockIdx.y;
   int tiles;
   group_rows(gr, min(e, gr.experts), 16, lo, hi, cnt, tiles);
+  clear = blockIdx.z ? hi - lo : cnt;
   if (gr.counts && e >= gr.experts) {
-    lo += (e - gr.experts) * kTailRows;
+    lo += ((e - gr.experts) * (int)gridDim.z + (int)blockIdx.z) * kTailRows;
     hi = min(hi, lo + kTailRows);
+    clear = 0;
   }
   return hi > lo;
 }

@@ -21,6 +21,8 @@
 // Measured without gain: a second barrier a step that lets the next step's operands be
 // read ahead (8% slower), tiles of 256 x 128, raised wave priority, every load of a step
 // before its products (20% slower), four waves of 128 x 128 (they spill).
+#include <algorithm>
+
 #include "common.h"
 #include "grouped.h"
 #include "launch.h"
@@ -291,9 +293,9 @@ __global__ __launch_bounds__(NT == 1 ? 512 : 256) void k_bf16_grouped_few(const 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), W = blockDim.x >> 6;
   const int n0 = (int)blockIdx.x * 16 * RT, cols = (int)min((int64_t)16 * RT, N - n0);
   const int e = blockIdx.y;
-  int lo, hi, cnt;
-  if (!few_rows(gr, lo, hi, cnt)) return;
-  if (blockIdx.z == 0) clear_rows(out + (int64_t)lo * N + n0, N, cnt, hi - lo, cols);
+  int lo, hi, cnt, clear;
+  if (!few_rows(gr, lo, hi, cnt, clear)) return;
+  clear_rows(out + (int64_t)lo * N + n0, N, clear, hi - lo, cols);
 
   // lane 16 g + 4 b + c loads, for j = 0..3, chunk 4 g + c (8 terms) of row 4 b + j; the
   // quad's exchange leaves chunk 4 g + j of row 4 b + c in register j
@@ -379,9 +381,9 @@ __global__ __launch_bounds__(512) void k_bf16_grouped_few_across(const uint16_t*
   typedef Tile<64, 64, true, 1> TileQ;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), W = blockDim.x >> 6;
   const int k0 = (int)blockIdx.x * 64, cols = (int)min((int64_t)64, K - k0), e = blockIdx.y;
-  int lo, hi, cnt;
-  if (!few_rows(gr, lo, hi, cnt)) return;
-  if (blockIdx.z == 0) clear_rows(drows + (int64_t)lo * K + k0, K, cnt, hi - lo, cols);
+  int lo, hi, cnt, clear;
+  if (!few_rows(gr, lo, hi, cnt, clear)) return;
+  clear_rows(drows + (int64_t)lo * K + k0, K, clear, hi - lo, cols);
   const int r = lane & 15, g = lane >> 4;
   char* own = lds + wave * 8192;
   constexpr int NT = 2;  // 32 rows at a time
@@ -579,7 +581,7 @@ int32_t product(const uint16_t* rows, int64_t r_cap, int64_t K, const uint16_t* 
   // each (512 blocks), 10.7 (13.0), 512 rows each (1024) 16.5 (13.3); 8 of 512 x 4096, 96 rows
   // (384) 26 (34), 128 rows (512) 34.5 (33.8), 256 rows (1024) 67 (34); 4 of 2048 x 2048, 64
   // rows (512) 18.2 (19.8), 128 rows (1024) 27 (20).
-  const int64_t groups = few_groups(r_cap, E, !counts), chunks = (mean + 31) / 32;
+  const int64_t chunks = (mean + 31) / 32;
   // Where the weights are read across, blocks are 64 columns wide, and many of them that
   // read each weight once are better off as tiles: 8 experts of 4096 x 4096, 16 rows, 63
   // (82); 32 of 4096 x 7168, 8 rows, 417 (386).  With more rows, up to 256 blocks: 4 experts
@@ -588,11 +590,13 @@ int32_t product(const uint16_t* rows, int64_t r_cap, int64_t K, const uint16_t* 
   const int64_t used = E < most ? E : most;  // experts with rows, at most
   const bool few = QT ? (mean <= 24 && used * ((N + 127) / 128) <= 1024) || E * ((N + 63) / 64) * chunks <= 256
                       : mean <= 24 || E * ((N + 31) / 32) * chunks <= 512;
+  // workgroups beside each other for one expert's rows: as many as the mean asks for,
+  // more (the loads may be uneven) where that leaves few
+  const int64_t spare = 1024 / (E * ((N + 63) / 64)), all = (most + 31) / 32;
+  const int64_t beside = std::clamp<int64_t>(std::max(chunks, std::min(spare, all)), 1, 32767);
+  const int64_t groups = few_groups(r_cap, E, !counts, beside);
   if (few && groups <= 65535) {
-    // workgroups beside each other for one expert's rows: as many as the mean asks for,
-    // more (the loads may be uneven) where that leaves few
-    const int64_t spare = 1024 / (E * ((N + 63) / 64)), all = (most + 31) / 32, z = chunks > spare ? chunks : spare < all ? spare : all;
-    const dim3 grid(1, (unsigned)groups, (unsigned)(z < 1 ? 1 : z < 32767 ? z : 32767));
+    const dim3 grid(1, (unsigned)groups, (unsigned)beside);
     if constexpr (QT) return product_few_across(rows, r_cap, K, weight, E, N, counts, offsets, grid, out, s);
     // up to 12 rows 16 at a time by eight waves: 4 rows 47 us and 64, 8 rows 320 and 312,
     // 16 rows 430 and 318

@@ -362,9 +362,9 @@ __global__ __launch_bounds__(256, 2) void k_mxfp4_grouped_few(
   float* red = reinterpret_cast<float*>(lds);  // [waves][RT][16 rows][16 columns]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), W = blockDim.x >> 6;
   const int n0 = (int)blockIdx.x * 16 * RT, cols = (int)min((int64_t)16 * RT, N - n0), e = blockIdx.y;
-  int lo, hi, cnt;
-  if (!few_rows(gr, lo, hi, cnt)) return;
-  if (blockIdx.z == 0) clear_rows(out + (int64_t)lo * N + n0, N, cnt, hi - lo, cols);
+  int lo, hi, cnt, clear;
+  if (!few_rows(gr, lo, hi, cnt, clear)) return;
+  clear_rows(out + (int64_t)lo * N + n0, N, clear, hi - lo, cols);
 
   // lane 16 g + 4 b + c loads, for j = 0..3, chunk 4 g + c (32 values) of row 4 b + j; the
   // quad's exchange leaves chunk 4 g + j of row 4 b + c in register j, lane group g's block
@@ -501,7 +501,6 @@ int32_t mx_product(const uint8_t* data, const uint8_t* scales, int64_t r_cap, in
                    const uint8_t* wscales, int64_t E, int64_t N, const int32_t* counts, const int32_t* offsets,
                    int64_t entries, uint16_t* out, hipStream_t s) {
   const int64_t most = entries < r_cap ? entries : r_cap, mean = (most + E - 1) / E;
-  const int64_t groups = few_groups(r_cap, E, !counts);
   // Up to 16 rows an expert (on average) by the kernel that streams the weights, MXFP4
   // rows 32 weight rows at a time, MXFP8 rows, which take twice the registers, 16: 32
   // experts of 4096 x 7168, 8 rows each, 99 us (tiles 137) and 153 (231); 16 rows 132
@@ -511,6 +510,7 @@ int32_t mx_product(const uint8_t* data, const uint8_t* scales, int64_t r_cap, in
   constexpr int RT = A8 ? 1 : 2;
   const int64_t chunks = mean > 16 ? (mean + 15) / 16 : 1;  // without entries, too: the rows are cleared
   const bool thin = K > 2048 && E * ((N + 16 * RT - 1) / (16 * RT)) * chunks <= 2048 && chunks <= 65535;
+  const int64_t groups = few_groups(r_cap, E, !counts, chunks);
   if ((mean <= 16 || thin) && groups <= 65535)
     return mx_few<RT, A8>(data, scales, r_cap, K, wcodes, wscales, E, N, counts, offsets,
                           dim3(1, (unsigned)groups, (unsigned)chunks), out, s);
