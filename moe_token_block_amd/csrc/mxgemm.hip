@@ -506,10 +506,15 @@ int32_t mx_product(const uint8_t* data, const uint8_t* scales, int64_t r_cap, in
   // experts of 4096 x 7168, 8 rows each, 99 us (tiles 137) and 153 (231); 16 rows 132
   // (140) and 223 (234); 32 rows of MXFP4 199 (148).
   // With more rows, too, where a long sum would be left to few tiles: a workgroup for
-  // each 16 rows.
+  // each 16 rows, up to 1024 of them (MXFP8 rows 2048).  4096 values, MXFP4 rows: 8 experts
+  // of width 512, 128 rows each (1024 workgroups), 14.8 us (tiles 17.7); one of 1024, 1024
+  // rows (2048), 22.9 (18.2); 4 of 4096, 60 rows (2048), 26 (17).  MXFP8 rows: the first of
+  // these (2048) 24.7 (31.6), the others (4096) 42 (32) and 44 (30).  8 of width 512, 64 rows
+  // each, of 2048 values 9.5 (MXFP8 rows; tiles 16.6) and 9.3 (10.5), of 1024 9.3 (11.2); 4
+  // of 256, 128 rows each, of 512 values alike.
   constexpr int RT = A8 ? 1 : 2;
   const int64_t chunks = mean > 16 ? (mean + 15) / 16 : 1;  // without entries, too: the rows are cleared
-  const bool thin = K > 2048 && E * ((N + 16 * RT - 1) / (16 * RT)) * chunks <= 2048 && chunks <= 65535;
+  const bool thin = K >= 1024 && E * ((N + 16 * RT - 1) / (16 * RT)) * chunks <= (A8 ? 2048 : 1024);
   const int64_t groups = few_groups(r_cap, E, !counts, chunks);
   if ((mean <= 16 || thin) && groups <= 65535)
     return mx_few<RT, A8>(data, scales, r_cap, K, wcodes, wscales, E, N, counts, offsets,
