@@ -1,9 +1,10 @@
-"""MXFP8 rows times MXFP4 weights where the terms cancel, so that no final rounding hides
+"""MXFP8 and MXFP4 rows times MXFP4 weights where the terms cancel, so that no final rounding hides
 what the sum loses.
 
 Every value is chosen so that each term is a multiple of 2^-7 and the terms' magnitudes
-add up to less than 2^17: FP32 holds any partial sum, in any order, and the result has
-to be the BF16 nearest to the exact sum (in float64, which holds it too), bit for bit."""
+add up to less than 2^17 (MXFP4 rows: of 2^-2, less than 2^22): FP32 holds any partial sum,
+in any order, and the result has to be the BF16 nearest to the exact sum (in float64,
+which holds it too), bit for bit."""
 
 import pytest
 import torch
@@ -77,6 +78,43 @@ def test_terms_that_cancel(dev, case):
         got = mtb.ep_mxfp4_grouped_gemm(data, s, wc, ws, plan)
         off = (got != want).nonzero()
         assert not len(off), (a, b, len(off), got.numel(), off[0].tolist(), got[tuple(off[0])].item(), want[tuple(off[0])].item())
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_four_bit_terms_that_cancel(dev, case):
+    """Up to 16 blocks of 32 at 2^9 of the others' scale, each with a pair of +-6 times 6 and else
+    0.5 times 0.5 or 1: 16 * (72 + 15) * 2^9 + k * 36 < 2^22 for k < 2^16."""
+    counts, k, n = CASES[case]
+    print(f"case {case}: {CASES[case]}", flush=True)
+    g = torch.Generator(device=dev).manual_seed(case)
+    plan, offsets, used = _plan(counts, 16, dev)
+    r, e = plan["r_cap"], len(counts)
+    ints = lambda lo, hi, *shape: torch.randint(lo, hi, shape, generator=g, device=dev).to(torch.uint8)  # noqa: E731
+    data = torch.zeros((r, k // 2), dtype=torch.uint8, device=dev)
+    s = torch.full((r, k // 32), 127, dtype=torch.uint8, device=dev)
+    wc = torch.empty((e, n, k // 2), dtype=torch.uint8, device=dev)
+    want = torch.zeros((r, n), dtype=torch.bfloat16, device=dev)
+    pack = lambda c: c[:, ::2] | (c[:, 1::2] << 4)  # noqa: E731
+    for i, (c, o) in enumerate(zip(counts, offsets)):
+        x, codes = ints(0, 16, c, k), ints(0, 16, n, k)
+        scales = torch.full((c, k // 32), 127, dtype=torch.uint8, device=dev)
+        for b in torch.randperm(k // 32, generator=g, device=dev)[:16].tolist():
+            at = slice(32 * b, 32 * b + 32)
+            x[:, at], codes[:, at] = 1 + 8 * ints(0, 2, c, 32), 1 + ints(0, 2, n, 32)
+            p, q = (32 * b + torch.randperm(32, generator=g, device=dev)[:2]).tolist()
+            x[:, p] = 7 + 8 * ints(0, 2, c)
+            x[:, q] = x[:, p] ^ 8
+            codes[:, p] = codes[:, q] = 7
+            scales[:, b] = 127 + 9
+        data[o:o + c], wc[i], s[o:o + c] = pack(x), pack(codes), scales
+        a = _values(x) * (scales.double() - 127).exp2().repeat_interleave(32, 1)
+        want[o:o + c] = (a @ _values(codes).T.contiguous()).float().bfloat16()
+    for a, b in ((0, 0), (-120, 118), (110, -110)):
+        ws = torch.full((e, n, k // 32), 127 + b, dtype=torch.uint8, device=dev)
+        got = mtb.ep_mxfp4_grouped_gemm(data, (s.int() + a).to(torch.uint8), wc, ws, plan)
+        exact = (want.double() * 2.0 ** (a + b)).bfloat16()  # a power of two: no rounding
+        off = (got != exact).nonzero()
+        assert not len(off), (a, b, len(off), got.numel(), off[0].tolist(), got[tuple(off[0])].item(), exact[tuple(off[0])].item())
 
 
 @pytest.mark.parametrize("counts,k,n", [([5, 16, 1], 96, 40), ([380, 420, 400], 160, 500), ([70] * 24, 96, 1100),
