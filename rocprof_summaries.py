@@ -2,7 +2,7 @@
 
 Run on a machine with an MI355X and rocprofv3, from the repository root; this
 process itself never touches the GPU (every GPU run is a rocprofv3 child), but as
-``expert-pass``, which is such a child.
+``expert-pass`` and ``library-rates``, which are such children.
 
   python rocprof_summaries.py counters [--configs 1,2,3,4,5] [--raw DIR]
       Per configuration, three rocprofv3 --pmc runs of `bench.py --counters-pass
@@ -33,7 +33,9 @@ process itself never touches the GPU (every GPU run is a rocprofv3 child), but a
       also three --pmc runs of it -> profiles/counters_expert_matvec.md.
   python rocprof_summaries.py products [--raw DIR]
       The same times of the grouped products and the norm, at the cases of
-      perf/more_operators.py -> profiles/kernel_times_products.md.
+      perf/more_operators.py, and the library's rates that their floors are priced at
+      (``library-rates``, a child too) -> profiles/kernel_times_products.md; for the
+      products also a --pmc run of each -> profiles/counters_products.md.
 """
 
 import argparse
@@ -441,6 +443,30 @@ def expert_pass(args):
     print(json.dumps({"case": args.case, "us": us, "graph_us": graph_us, "loads": loads, **ops.work(case)}), flush=True)
 
 
+def library_rates(args):
+    """The rates that the products' floors are priced at: torch's BF16 products of 8192^3 with both operands along
+    the sum, one and both across it, and a copy of 1 GiB; the median of seven runs of 20 calls after 0.5 s of them."""
+    import torch
+    a, b = (torch.randn(8192, 8192, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    x = torch.empty(1 << 30, dtype=torch.uint8, device="cuda")
+    y, c = torch.empty_like(x), torch.empty_like(a)
+    got = {}
+    for name, work, f in (("along, along TFLOP/s", 2 * 8192.0 ** 3 / 1e12, lambda: torch.mm(a, b.T, out=c)),
+                          ("along, across TFLOP/s", 2 * 8192.0 ** 3 / 1e12, lambda: torch.mm(a, b, out=c)),
+                          ("across, across TFLOP/s", 2 * 8192.0 ** 3 / 1e12, lambda: torch.mm(a.T, b, out=c)),
+                          ("copy TB/s", 2.0 * (1 << 30) / 1e12, lambda: y.copy_(x))):
+        times, t1 = [], time.perf_counter()
+        while len(times) < 7:
+            t0 = time.perf_counter()
+            for _ in range(20):
+                f()
+            torch.cuda.synchronize()
+            if time.perf_counter() - t1 > 0.5:  # the clock has settled
+                times.append((time.perf_counter() - t0) / 20)
+        got[name] = work / sorted(times)[3]
+    print(json.dumps({"rates": got}), flush=True)
+
+
 def _expert_run(tool, case, out, settle, products=False):
     """One profiled run of the child; its line, the trace's directory and the command as shown."""
     child = ["rocprof_summaries.py", "expert-pass", "--settle-s", str(settle)] + (["--products"] if products else [])
@@ -500,10 +526,50 @@ def _times(args, raw, cases, sources, title, name, products=False):
     return head
 
 
+def _case_counters(raw, case, groups, shown, products=False):
+    """One run a group of counters: the child's line and each counter's sum of a pass."""
+    got = {}
+    for g in groups:
+        out = os.path.join(raw, f"pmc_{case['name']}_{g[0]}")
+        line, cmd = _expert_run(["--pmc"] + list(g), case["name"], out, 0.0, products)
+        if cmd not in shown:
+            shown.append(cmd)
+        rows = _between_marks(list(csv.DictReader(open(os.path.join(out, "run_counter_collection.csv")))),
+                              "Kernel_Name", lambda r: int(r["Dispatch_Id"]))
+        for r in rows:
+            got[r["Counter_Name"]] = got.get(r["Counter_Name"], 0.0) + float(r["Counter_Value"]) / EXPERT_PASSES
+    return line, got
+
+
 def products(args):
     raw = args.raw or tempfile.mkdtemp(prefix="mtb_products_")
-    _times(args, raw, product_cases()[1], PRODUCT_SOURCES, "Times of the grouped products and of the norm",
-           "kernel_times_products.md", products=True)
+    cases = product_cases()[1]
+    head = _times(args, raw, cases, PRODUCT_SOURCES, "Times of the grouped products and of the norm",
+                  "kernel_times_products.md", products=True)
+    text = run([sys.executable, os.path.join(ROOT, "rocprof_summaries.py"), "library-rates"], 150)
+    rates = json.loads(next(ln for ln in text.splitlines() if ln.startswith('{"rates"')))["rates"]
+    with open(os.path.join(args.out_dir, "kernel_times_products.md"), "a") as fh:
+        fh.write("\nRates of torch's BF16 products of 8192 x 8192 matrices (which operands lie along the sum, which across) "
+                 "and of its copy of 1 GiB, the median of seven runs of 20 calls after 0.5 s of them "
+                 "(`python3 rocprof_summaries.py library-rates`): "
+                 + "; ".join(f"{k} {v:.0f}" if v > 100 else f"{k} {v:.2f}" for k, v in rates.items()) + ".\n")
+    shown, md = [], []
+    for c in [c for c in cases if c["op"] in ("gemm", "dgrad", "wgrad", "mx")]:
+        line, got = _case_counters(raw, c, EXPERT_GROUPS[2:], shown, products=True)
+        md.append(f"| {c['name']} | {got['SQ_INSTS_VALU']:.4g} | {got['SQ_ACTIVE_INST_VALU']:.4g} | "
+                  f"{got['SQ_VALU_MFMA_BUSY_CYCLES']:.4g} | {got['SQ_BUSY_CU_CYCLES']:.4g} | "
+                  f"{got['SQ_VALU_MFMA_BUSY_CYCLES'] / got['SQ_BUSY_CU_CYCLES'] / 4:.2f} | {got['SQ_INSTS_LDS']:.4g} | "
+                  f"{got['SQ_LDS_BANK_CONFLICT']:.4g} | {got['SQ_WAIT_INST_ANY'] / got['SQ_WAVE_CYCLES']:.2f} | "
+                  f"{line['flops'] / 1e9:.1f} |")
+    doc = ["# Counters of the grouped products", ""] + head + shown + ["```", "",
+           f"Per pass, {EXPERT_PASSES} passes over three input sets in turn; summed over the counter's dimensions.  VALU "
+           "wave-instructions, active VALU cycles and busy MFMA cycles of all SIMDs, busy cycles of all CUs; the matrix "
+           "units' busy share of those (four SIMDs a CU); LDS instructions and conflict cycles; the share of a wave's "
+           "cycles in which it waits for an instruction to issue or return; GFLOP.", "",
+           "| case | VALU | VALU cycles | MFMA cycles | CU cycles | MFMA busy | LDS | LDS conflicts | waiting | GFLOP |",
+           "|---|---|---|---|---|---|---|---|---|---|"]
+    with open(os.path.join(args.out_dir, "counters_products.md"), "w") as fh:
+        fh.write("\n".join(doc + md) + "\n")
 
 
 def expert(args):
@@ -514,16 +580,7 @@ def expert(args):
     ref = json.load(open(os.path.join(ROOT, "profiles", "counters.json")))["copy_reference"]
     shown, md = [], []
     for c in [c for c in cases if c["op"] == "matvec" and c["n"] * c["k"] > 1 << 22]:
-        got = {}
-        for g in EXPERT_GROUPS:
-            out = os.path.join(raw, f"pmc_{c['name']}_{g[0]}")
-            line, cmd = _expert_run(["--pmc"] + list(g), c["name"], out, 0.0)
-            if cmd not in shown:
-                shown.append(cmd)
-            rows = _between_marks(list(csv.DictReader(open(os.path.join(out, "run_counter_collection.csv")))),
-                                  "Kernel_Name", lambda r: int(r["Dispatch_Id"]))
-            for r in rows:
-                got[r["Counter_Name"]] = got.get(r["Counter_Name"], 0.0) + float(r["Counter_Value"]) / EXPERT_PASSES
+        line, got = _case_counters(raw, c, EXPERT_GROUPS, shown)
         md.append(f"| {c['name']} | {line['bytes'] / 1e6:.1f} | {got['TCC_MISS_sum'] * 128 / 1e6:.1f} | "
                   f"{got['FETCH_SIZE'] * 1024 * ref['FETCH_SIZE'] / 1e6:.1f} | "
                   f"{got['TCC_EA0_RDREQ_DRAM_sum'] * ref['TCC_EA0_RDREQ_DRAM_sum'] / 1e6:.1f} | "
@@ -546,7 +603,8 @@ def expert(args):
 
 def main():
     p = argparse.ArgumentParser()
-    p.add_argument("what", choices=["counters", "kernels", "trace", "expert", "products", "expert-pass"])
+    p.add_argument("what", choices=["counters", "kernels", "trace", "expert", "products", "expert-pass",
+                                    "library-rates"])
     p.add_argument("--case", default=None, help="expert-pass: the case's name")
     p.add_argument("--products", action="store_true", help="expert-pass: a case of perf/more_operators.py")
     p.add_argument("--timed", action="store_true", help="expert-pass: time the passes too, eager and in a graph")
@@ -557,8 +615,8 @@ def main():
     p.add_argument("--steps", type=int, default=20)
     p.add_argument("--out-dir", default=os.path.join(ROOT, "profiles"), help="where the summaries go")
     args = p.parse_args()
-    if args.what == "expert-pass":
-        return expert_pass(args)
+    if args.what in ("expert-pass", "library-rates"):
+        return {"expert-pass": expert_pass, "library-rates": library_rates}[args.what](args)
     args.out_dir = os.path.abspath(args.out_dir)
     os.makedirs(args.out_dir, exist_ok=True)
     if args.raw:
