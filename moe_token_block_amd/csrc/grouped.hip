@@ -11,13 +11,14 @@
 // transposing read turns into the instruction's operand.  For few rows the weights'
 // bytes are the time, and kernels of their own stream them.
 //
-// Measured (large library products of the same kinds reach 1430, 1250 and 1100
+// Measured (large library products of the same kinds reach 1620, 1410 and 1220
 // TFLOP/s): 131072 rows of 32 experts, 7168 x 4096, 6.6 to 6.9 ms, 1120 to 1170
 // TFLOP/s; the rows' gradient of 8192 uneven rows, 8 experts of 4096 x 4096, 312 us,
 // 880; the weights' of 65536 rows, 16 experts of 4096 x 4096, 1.79 to 1.88 ms, 1170 to
-// 1230.  The matrix unit is busy about half of the time; the rest are the steps'
-// barriers with the first LDS reads behind them, and the first loads and the stores of
-// a tile, which nothing else on the CU overlaps (128 KB of LDS, 240 registers a lane).
+// 1230.  The matrix units are busy in 0.57 to 0.64 of the CUs' busy cycles, at clocks
+// below 1.8 GHz (the large product); the rest are the steps' barriers with the first LDS
+// reads behind them, and the first loads and the stores of a tile, which nothing else on
+// the CU overlaps (128 KB of LDS, 240 registers a lane).
 // Measured without gain: a second barrier a step that lets the next step's operands be
 // read ahead (8% slower), tiles of 256 x 128, raised wave priority, every load of a step
 // before its products (20% slower), four waves of 128 x 128 (they spill).
@@ -373,7 +374,8 @@ __global__ __launch_bounds__(NT == 1 ? 512 : 256) void k_bf16_grouped_few(const 
 // drows for experts with few rows: as k_bf16_grouped_few, but the weights' rows are the
 // sum's terms: a wave's 64 of them by 64 columns go through LDS of its own, whose
 // transposing read makes the instruction's operand.  One token, 2 of 8 experts of 4096 x
-// 2048: 16.5 us for 34 MB; 128 rows, 8 experts of 4096 x 4096: 63 us for 270 MB.
+// 2048 (width first): 14.2 us for 34 MB, 64 blocks with work and 8 steps a wave; of 2048 x
+// 4096, 128 blocks and 4 steps, 10.5 us; 128 rows, 8 experts of 4096 x 4096: 61 us for 270 MB.
 __global__ __launch_bounds__(512) void k_bf16_grouped_few_across(const uint16_t* __restrict__ dout, int64_t N,
                                                                  const uint16_t* __restrict__ weight, int64_t K,
                                                                  Groups gr, uint16_t* __restrict__ drows) {
